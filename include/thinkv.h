@@ -37,12 +37,13 @@
  *   - Device-detected errors (bad token/sequence data, exhausted page pool,
  *     full block table, a bounded wait that ran out) are written to the
  *     cache's sticky `status` word: the first error wins and later errors do
- *     not overwrite it.  While *status != 0, append and evict do nothing;
+ *     not overwrite it.  While *status != 0, append, evict, release and fork
+ *     do nothing;
  *     decode still runs (it only reads state that every operation leaves
  *     consistent).  thinkv_get_status / thinkv_clear_status read and reset it.
  *   - Nothing traps or spins without a bound.
- *   - Small appends, small evicts and decode launch their kernels with
- *     programmatic stream serialisation: a kernel may start while the
+ *   - Small appends, small evicts, release, fork and decode launch their
+ *     kernels with programmatic stream serialisation: a kernel may start while the
  *     previous kernel on the stream is finishing.  Before waiting for that
  *     kernel it reads only the call's own input arrays (token ids,
  *     positions, tags, K/V rows, budgets, sequence ids); cache state is read
@@ -140,7 +141,13 @@ enum { THINKV_FMT_INT = 0, THINKV_FMT_FLOAT = 1 };
  *                 swap-with-last when it loses its last one.
  *   live_index    int32 [max_seqs][max_blocks_per_seq]  position of an entry
  *                 in live_list, -1 if absent.    num_live int32 [max_seqs].
- *   page_bump     int32 [3]              pages handed out per class pool
+ *   page_bump     int32 [6 + pool_pages[0] + pool_pages[1] + pool_pages[2]]
+ *                 [0, 3): pages ever handed out per class pool; [3, 6):
+ *                 released pages per class waiting to be handed out again;
+ *                 then one stack of released page ids per class, pool_pages[c]
+ *                 entries each, class after class.  A pool grants the top of
+ *                 its released stack while it has one, else the page numbered
+ *                 page_bump[c]++.
  *   status        int32 [1]              sticky device status (thinkv_status)
  *
  * Page-head block of a class with b = bits[c] < 16 (d = head_dim, G =
@@ -227,7 +234,7 @@ THINKV_API size_t thinkv_append_workspace_bytes(const thinkv_layout* L, int32_t 
  * within the run); positions should also grow across calls (they order the
  * tokens of a sequence).
  * Each token takes the top slot of its (sequence, class) free stack; when that
- * stack is empty the class pool grants the next page (page_bump[c]), a table
+ * stack is empty the class pool grants the next page (page_bump above), a table
  * entry {page, class, mask 0} is appended, slots 15..1 are pushed (slot 1 on
  * top) and slot 0 is used.  The token's K and V are quantised at bits[class]
  * into the slot, its live bit and slot_pos are set, its slot id is pushed on
@@ -382,6 +389,42 @@ THINKV_API size_t thinkv_compact_workspace_bytes(int32_t n_seqs, int32_t max_tok
 THINKV_API int thinkv_compact(const thinkv_cache* src, const thinkv_cache* dst, int32_t n_seqs,
                               const int32_t* seq, int32_t max_tokens, void* workspace,
                               size_t workspace_bytes, void* stream);
+
+/* Workspace bytes thinkv_release and thinkv_fork need for n_seqs sequences. */
+THINKV_API size_t thinkv_turnover_workspace_bytes(const thinkv_layout* L, int32_t n_seqs);
+
+/* Release: the sequences seq[0..n_seqs) (distinct) end.  Their pages go onto
+ * the released stacks of their class pools, the last page of the call (in call
+ * order, then table order) first, so that the call's pages are granted again
+ * in that order; the slot_pos of those pages become -1, the sequences' table
+ * entries 0 and live_index -1, and each sequence is empty, as after
+ * thinkv_cache_reset (the pool bytes stay as they are).  An empty sequence may
+ * be released.  tbe: NULL, or the cache's TBE state, whose segments of the
+ * sequences are dropped; pass it if the sequences were driven by
+ * thinkv_evict_tbe.
+ * A repeated or out-of-range id -> *status = INVALID and nothing changes;
+ * while *status != 0 the call does nothing.  n_seqs <= max_seqs.
+ * workspace: device, >= thinkv_turnover_workspace_bytes(L, n_seqs) bytes,
+ * zero-filled once before its first use (its first 4 bytes are an arrival
+ * counter that every call leaves at zero).  Calls that share a workspace must
+ * not overlap on the GPU.  Two kernels. */
+THINKV_API int thinkv_release(const thinkv_cache* cache, const thinkv_tbe* tbe, int32_t n_seqs,
+                              const int32_t* seq, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Fork: sequence dst[i] becomes a copy of src[i], for i < n_seqs.  The
+ * destinations are distinct and hold no page (never used, or released), and
+ * none is also a source; a source may repeat.  dst[i] is granted as many pages
+ * of each class as src[i] holds, in call order and table order (page_bump
+ * above); the pages' bytes and slot positions, the table, the free stacks, the
+ * FIFO windows and counters, the live list and, with tbe, the TBE segments are
+ * those of the source.  Afterwards the two are independent: each appends,
+ * evicts and decodes on its own.
+ * Bad ids or a destination that holds a page -> *status = INVALID, an exhausted
+ * pool -> OUT_OF_PAGES, both with nothing changed; while *status != 0 the call
+ * does nothing.  tbe, workspace: as for thinkv_release.  Two kernels. */
+THINKV_API int thinkv_fork(const thinkv_cache* cache, const thinkv_tbe* tbe, int32_t n_seqs,
+                           const int32_t* src, const int32_t* dst, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /* Workspace bytes thinkv_decode_attention needs on the CURRENT device. */
 THINKV_API size_t thinkv_decode_workspace_bytes(const thinkv_layout* L, int32_t n_seqs, int32_t topk);

@@ -38,6 +38,7 @@ EXPORTED = [
     "thinkv_tbe_buffer_bytes", "thinkv_tbe_reset", "thinkv_tbe_workspace_bytes", "thinkv_evict_tbe",
     "thinkv_evict_slots_workspace_bytes", "thinkv_evict_slots",
     "thinkv_compact_workspace_bytes", "thinkv_compact",
+    "thinkv_turnover_workspace_bytes", "thinkv_release", "thinkv_fork",
 ]
 
 TBE_BUFFERS = ["seg", "nseg", "settled"]
@@ -130,6 +131,12 @@ def lib():
                                          P, SZ, P]
             L.thinkv_compact.restype = C.c_int
             L.thinkv_classify_thoughts.restype = C.c_int
+            L.thinkv_turnover_workspace_bytes.argtypes = [C.POINTER(Layout), I32]
+            L.thinkv_turnover_workspace_bytes.restype = SZ
+            L.thinkv_release.argtypes = [C.POINTER(CacheStruct), C.POINTER(TbeStruct), I32, P, P, SZ, P]
+            L.thinkv_release.restype = C.c_int
+            L.thinkv_fork.argtypes = [C.POINTER(CacheStruct), C.POINTER(TbeStruct), I32, P, P, P, SZ, P]
+            L.thinkv_fork.restype = C.c_int
             L.thinkv_status_string.argtypes = [I32]
             L.thinkv_status_string.restype = C.c_char_p
             _lib = L
@@ -180,12 +187,15 @@ class ThinKVCache:
 
     Buffers are torch tensors owned by this object; the C ABI sees raw device
     pointers.  ``bits`` are the code widths of R, E, T (default 8/4/2).
+    ``buffers``: a cache that exists already (contiguous tensors on ``device``,
+    by the names in ``BUFFERS``, and in ``TBE_BUFFERS`` with ``tbe``); it is
+    taken over as it stands, not reset.
     """
 
     def __init__(self, num_q_heads: int, num_kv_heads: int, head_dim: int, group_size: int,
                  bits: Sequence[int], max_seqs: int, max_blocks_per_seq: int,
                  pool_pages: Sequence[int], device: str = "cuda", tbe: bool = False,
-                 fmt: Sequence[int] = (0, 0, 0)):
+                 fmt: Sequence[int] = (0, 0, 0), buffers: Optional[dict] = None):
         self.layout = make_layout(num_q_heads, num_kv_heads, head_dim, group_size, bits,
                                   max_seqs, max_blocks_per_seq, pool_pages, fmt)
         self.fmt = tuple(int(f) for f in fmt)
@@ -199,8 +209,7 @@ class ThinKVCache:
         self.buf = {}
         for i, name in enumerate(BUFFERS):
             nbytes = int(L.thinkv_buffer_bytes(C.byref(self.layout), i))
-            self.buf[name] = (torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-                              if nbytes > 0 else None)
+            self.buf[name] = self._buffer(name, nbytes, buffers)
         self.cs = CacheStruct()
         self.cs.L = self.layout
         for c, n in enumerate("RET"):
@@ -214,9 +223,22 @@ class ThinKVCache:
             self.tbe_buf = {}
             for i, name in enumerate(TBE_BUFFERS):
                 nbytes = int(L.thinkv_tbe_buffer_bytes(C.byref(self.layout), i))
-                self.tbe_buf[name] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+                self.tbe_buf[name] = self._buffer(name, nbytes, buffers)
             self.tbe = TbeStruct(*[_ptr(self.tbe_buf[n]) for n in TBE_BUFFERS])
-        self.reset()
+        if buffers is None:
+            self.reset()
+
+    def _buffer(self, name: str, nbytes: int, given: Optional[dict]) -> Optional[torch.Tensor]:
+        if given is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes > 0 else None
+        t = given.get(name)
+        if nbytes == 0:
+            return t
+        if t is None or not t.is_contiguous() or t.numel() * t.element_size() != nbytes:
+            raise ThinkvError(ERR_INVALID, f"buffer {name}: a contiguous tensor of {nbytes} bytes is needed")
+        if t.device.type != self.device.type or self.device.index not in (None, t.device.index):
+            raise ThinkvError(ERR_INVALID, f"buffer {name} is on {t.device}, not on {self.device}")
+        return t
 
     # -- helpers --
     def page_head_bytes(self, c: int) -> int:
@@ -320,6 +342,63 @@ class ThinKVCache:
                                     int(max_tokens), _ptr(ws), ws.numel(), _stream(stream)),
                "compact")
 
+    def release(self, seq: torch.Tensor, stream=None):
+        """The sequences `seq` (distinct) end: their pages go back to the pools."""
+        n = int(seq.numel())
+        self._expect(seq, torch.int32, n)
+        if n == 0:
+            return
+        with self._guard():
+            st = self._stream_here(stream)
+            ws = self._counter_workspace("turnover", self._turnover_bytes(n), st)
+            _check(lib().thinkv_release(C.byref(self.cs), self._tbe_ref(), n, _ptr(seq), _ptr(ws), ws.numel(),
+                                        st.cuda_stream), "release")
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
+        """Sequence dst[i] (empty; distinct) becomes a copy of src[i]."""
+        n = int(src.numel())
+        self._expect(src, torch.int32, n)
+        self._expect(dst, torch.int32, n)
+        if n == 0:
+            return
+        with self._guard():
+            st = self._stream_here(stream)
+            ws = self._counter_workspace("turnover", self._turnover_bytes(n), st)
+            _check(lib().thinkv_fork(C.byref(self.cs), self._tbe_ref(), n, _ptr(src), _ptr(dst), _ptr(ws),
+                                     ws.numel(), st.cuda_stream), "fork")
+
+    def _turnover_bytes(self, n: int) -> int:
+        nbytes = int(lib().thinkv_turnover_workspace_bytes(C.byref(self.layout), n))
+        if nbytes == 0:
+            raise ThinkvError(ERR_INVALID, f"{n} sequences in one call of a cache of {self.max_seqs}")
+        return nbytes
+
+    def _tbe_ref(self):
+        return None if self.tbe is None else C.byref(self.tbe)
+
+    def _expect(self, t: torch.Tensor, dtype, numel: int):
+        assert t.dtype == dtype and t.is_contiguous() and t.numel() == numel
+        assert t.device == self.buf["status"].device, f"tensor on {t.device}, cache on {self.device}"
+
+    def _guard(self):
+        # kernels are launched on the cache's device, whichever is current
+        return torch.cuda.device(self.buf["status"].device)
+
+    def _stream_here(self, stream):
+        return stream if stream is not None else torch.cuda.current_stream()
+
+    def _counter_workspace(self, key: str, nbytes: int, stream) -> torch.Tensor:
+        """A workspace whose arrival counter is zeroed once, in the order of `stream`.  Its first
+        use cannot be inside a graph capture: the zero fill would only run when the graph does."""
+        t = self._ws.get(key)
+        if t is None or t.numel() < nbytes:
+            if torch.cuda.is_current_stream_capturing():
+                raise ThinkvError(ERR_WORKSPACE, f"{key}: run the call once before capturing it")
+            with torch.cuda.stream(stream):
+                t = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.buf["status"].device)
+            self._ws[key] = t
+        return t
+
     def decode_workspace_bytes(self, n: int, topk: int = 0) -> int:
         return int(lib().thinkv_decode_workspace_bytes(C.byref(self.layout), n, topk))
 
@@ -360,6 +439,9 @@ class ThinKVCache:
     def snapshot(self) -> dict:
         ns, nb = self.max_seqs, self.max_blocks
         cap = nb * PAGE
+        bump = self._host("page_bump", np.int32, (6 + sum(self.pool_pages),))
+        start = 6 + np.concatenate([[0], np.cumsum(self.pool_pages)])
+        released = [bump[start[c]:start[c] + bump[3 + c]].copy() for c in range(3)]
         st = {
             "table": self._host("block_table", np.uint64, (ns, nb)),
             "num_blocks": self._host("num_blocks", np.int32, (ns,)),
@@ -372,7 +454,8 @@ class ThinKVCache:
             "live_list": self._host("live_list", np.uint64, (ns, nb)),
             "live_index": self._host("live_index", np.int32, (ns, nb)),
             "num_live": self._host("num_live", np.int32, (ns,)),
-            "page_bump": self._host("page_bump", np.int32, (3,)),
+            "page_bump": bump[:3],
+            "released": released,          # per class, the next page to be granted last
             "slot_pos": [self._host(f"slot_pos_{n}", np.int32, (self.pool_pages[c], PAGE))
                          for c, n in enumerate("RET")],
         }

@@ -152,7 +152,8 @@ size_t thinkv_buffer_bytes(const thinkv_layout* L, int32_t which) {
     case THINKV_BUF_LIVE_LIST: return ns * nb * 8;
     case THINKV_BUF_LIVE_INDEX: return ns * nb * 4;
     case THINKV_BUF_NUM_LIVE: return ns * 4;
-    case THINKV_BUF_PAGE_BUMP: return 3 * 4;
+    case THINKV_BUF_PAGE_BUMP:   // counters, then a stack of released pages per class
+      return 4 * (6 + (size_t)L->pool_pages[0] + (size_t)L->pool_pages[1] + (size_t)L->pool_pages[2]);
     case THINKV_BUF_STATUS: return 4;
     default: return 0;
   }
@@ -176,7 +177,7 @@ int thinkv_cache_reset(const thinkv_cache* C, void* stream) {
   zero(C->fifo_tail, THINKV_BUF_FIFO_TAIL);
   zero(C->live_count, THINKV_BUF_LIVE_COUNT);
   zero(C->num_live, THINKV_BUF_NUM_LIVE);
-  zero(C->page_bump, THINKV_BUF_PAGE_BUMP);
+  if (e == cudaSuccess) e = cudaMemsetAsync(C->page_bump, 0, 6 * 4, s);   // the counters; the stacks are empty
   zero(C->status, THINKV_BUF_STATUS);
   minus_one(C->live_index, THINKV_BUF_LIVE_INDEX);
   for (int c = 0; c < 3; ++c)
@@ -342,6 +343,38 @@ int thinkv_compact(const thinkv_cache* src, const thinkv_cache* dst, int32_t n, 
   if (sms <= 0) return THINKV_ERR_CUDA;
   return cuda_status(launch_compact(view_of(src), view_of(dst), n, seq, max_tokens, workspace, sms,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t thinkv_turnover_workspace_bytes(const thinkv_layout* L, int32_t n_seqs) {
+  if (!layout_ok(L) || n_seqs < 0 || n_seqs > L->max_seqs) return 0;
+  return turnover_workspace_bytes(*L, n_seqs);
+}
+
+int thinkv_release(const thinkv_cache* C, const thinkv_tbe* T, int32_t n, const int32_t* seq,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cache_ok(C) || (T && !tbe_ok(T)) || n < 0 || n > C->L.max_seqs) return THINKV_ERR_INVALID;
+  if (n == 0) return THINKV_OK;
+  if (!seq || !aligned(seq, 4)) return THINKV_ERR_INVALID;
+  if (workspace && !aligned(workspace, 16)) return THINKV_ERR_INVALID;
+  if (!workspace || workspace_bytes < turnover_workspace_bytes(C->L, n)) return THINKV_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return THINKV_ERR_CUDA;
+  return cuda_status(launch_release(view_of(C), n, seq, T ? T->nseg : nullptr, T ? T->settled : nullptr,
+                                    workspace, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int thinkv_fork(const thinkv_cache* C, const thinkv_tbe* T, int32_t n, const int32_t* src,
+                const int32_t* dst, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cache_ok(C) || (T && !tbe_ok(T)) || n < 0 || n > C->L.max_seqs) return THINKV_ERR_INVALID;
+  if (n == 0) return THINKV_OK;
+  if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4)) return THINKV_ERR_INVALID;
+  if (workspace && !aligned(workspace, 16)) return THINKV_ERR_INVALID;
+  if (!workspace || workspace_bytes < turnover_workspace_bytes(C->L, n)) return THINKV_ERR_WORKSPACE;
+  const int sms = num_sms_current();
+  if (sms <= 0) return THINKV_ERR_CUDA;
+  return cuda_status(launch_fork(view_of(C), n, src, dst, T ? reinterpret_cast<int4*>(T->seg) : nullptr,
+                                 T ? T->nseg : nullptr, T ? T->settled : nullptr, workspace, sms,
+                                 static_cast<cudaStream_t>(stream)));
 }
 
 size_t thinkv_decode_workspace_bytes(const thinkv_layout* L, int32_t n_seqs, int32_t topk) {

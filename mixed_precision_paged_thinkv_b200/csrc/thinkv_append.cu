@@ -23,6 +23,7 @@
 #include "thinkv_common.cuh"
 #include "thinkv_evict_seq.cuh"
 #include "thinkv_internal.h"
+#include "thinkv_pages.cuh"
 
 namespace thinkv {
 
@@ -67,8 +68,9 @@ __device__ int block_exclusive_scan(int v, int* sh, int* total) {
 }
 
 // Slot assignment of one sequence run (one warp): tokens start..start+len-1
-// of sequence s, cnt[c] tokens of class c, new pages of class c numbered from
-// page_base[c] on.  Each token takes the top of its (sequence, class) free
+// of sequence s, cnt[c] tokens of class c, new pages of class c with virtual
+// numbers from page_base[c] on (bump: the call's starting page_bump; see
+// thinkv_pages.cuh).  Each token takes the top of its (sequence, class) free
 // stack, or the next slot of a new page; table entries, slot positions, FIFO
 // pushes, live-list joins, the final free stacks and the sequence counters
 // are written, and tok_slot[i] gets token i's pool slot (page * 16 + slot).
@@ -76,9 +78,9 @@ __device__ int block_exclusive_scan(int v, int* sh, int* total) {
 // null, holds s's counters already loaded: free_top[3], fifo_tail[3],
 // num_blocks, num_live, live_count.
 __device__ void assign_run(const CacheView& C, int s, int start, int len, const int (&cnt_in)[3],
-                           const int (&page_base)[3], const int32_t* __restrict__ pos,
-                           const uint8_t* __restrict__ tag, int32_t* tok_slot,
-                           const int* st = nullptr) {
+                           const int (&page_base)[3], const int* bump,
+                           const int32_t* __restrict__ pos, const uint8_t* __restrict__ tag,
+                           int32_t* tok_slot, const int* st = nullptr) {
   const int lane = threadIdx.x & 31;
   const int nb_max = C.L.max_blocks_per_seq;
   const int64_t cap = (int64_t)nb_max * kPage;
@@ -130,7 +132,7 @@ __device__ void assign_run(const CacheView& C, int s, int start, int len, const 
       } else {
         entry = mine ? entry_from : last_entry[c];
         slot = slot_new;
-        page = (uint32_t)(page_base[c] + j);
+        page = (uint32_t)granted_page(C, c, page_base[c] + j, bump[c]);
       }
     }
     // live-list candidates: granted entries, and reused entries with no live
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(kAssignThreads, 1)
       int g = r < R ? ws.runs[r].grants[cc] : 0;
       int total;
       int excl = block_exclusive_scan(g, sh, &total);
-      if (r < R) ws.runs[r].page_base[cc] = C.page_bump[cc] + carry + excl;
+      if (r < R) ws.runs[r].page_base[cc] = C.page_bump[cc] - C.page_bump[3 + cc] + carry + excl;
       carry += total;
     }
     if (tid == 0) s_total[cc] = carry;
@@ -295,7 +297,8 @@ __global__ void __launch_bounds__(kAssignThreads, 1)
     int err = 0;
     if (s_blocks_bad) err = THINKV_ERR_OUT_OF_BLOCKS;
     for (int cc = 0; cc < 3; ++cc)
-      if ((int64_t)C.page_bump[cc] + s_total[cc] > C.L.pool_pages[cc]) err = THINKV_ERR_OUT_OF_PAGES;
+      if (!pool_has(C, cc, C.page_bump[cc], C.page_bump[3 + cc], s_total[cc]))
+        err = THINKV_ERR_OUT_OF_PAGES;
     s_err = err;
     if (err) set_status(C.status, err);
   }
@@ -305,11 +308,11 @@ __global__ void __launch_bounds__(kAssignThreads, 1)
   // ---- phase 4: slot assignment, warp per run ------------------------------
   for (int r = warp; r < R; r += kAssignWarps) {
     const RunInfo ri = ws.runs[r];
-    assign_run(C, ri.seq, ri.start, ri.len, ri.cnt, ri.page_base, pos, tag, ws.tok_slot);
+    assign_run(C, ri.seq, ri.start, ri.len, ri.cnt, ri.page_base, C.page_bump, pos, tag, ws.tok_slot);
   }
   __syncthreads();
   if (tid == 0) {
-    for (int cc = 0; cc < 3; ++cc) C.page_bump[cc] += s_total[cc];
+    for (int cc = 0; cc < 3; ++cc) take_pages(C, cc, C.page_bump[cc], C.page_bump[3 + cc], s_total[cc]);
     __threadfence();
     *ws.ok = 1;
   }
@@ -602,7 +605,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   __shared__ int32_t tok_slot[kSmallAppend];      // pool slots of this CTA's run
   __shared__ ScatterSmem<D> sm[kSmallWarps];
   __shared__ int sh[8 * kSmallWarps];
-  __shared__ int s_err, s_base[3], s_total[3], s_bump[3], s_blocks_bad;
+  __shared__ int s_err, s_base[3], s_total[3], s_bump[3], s_released[3], s_blocks_bad;
   const int tid = threadIdx.x, warp = tid >> 5;
   const int max_seqs = C.L.max_seqs, nb_max = C.L.max_blocks_per_seq, H = C.L.num_kv_heads;
   const int b = blockIdx.x;                       // the run this CTA owns (if any)
@@ -682,7 +685,10 @@ __global__ void __launch_bounds__(kSmallThreads)
     if (*C.status != 0) s_err = -1;
     s_blocks_bad = 0;
 #pragma unroll
-    for (int c = 0; c < 3; ++c) s_bump[c] = C.page_bump[c];
+    for (int c = 0; c < 3; ++c) {
+      s_bump[c] = C.page_bump[c];
+      s_released[c] = C.page_bump[3 + c];
+    }
   }
   int R;
   const int rbase = small_exclusive_scan(nstart, sh, &R);   // (its barriers publish s_err)
@@ -738,14 +744,14 @@ __global__ void __launch_bounds__(kSmallThreads)
     if (tid == 0) {
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
-        s_base[c] = s_bump[c] + acc[c];
+        s_base[c] = s_bump[c] - s_released[c] + acc[c];
         s_total[c] = acc[3 + c];
       }
       int err = 0;
       if (s_blocks_bad) err = THINKV_ERR_OUT_OF_BLOCKS;
 #pragma unroll
       for (int c = 0; c < 3; ++c)
-        if ((int64_t)s_bump[c] + acc[3 + c] > C.L.pool_pages[c]) err = THINKV_ERR_OUT_OF_PAGES;
+        if (!pool_has(C, c, s_bump[c], s_released[c], acc[3 + c])) err = THINKV_ERR_OUT_OF_PAGES;
       s_err = err;
     }
     __syncthreads();
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     if (warp == 0) {
       const int cnt[3] = {r_cnt[b * 3 + 0], r_cnt[b * 3 + 1], r_cnt[b * 3 + 2]};
       const int base[3] = {s_base[0], s_base[1], s_base[2]};
-      assign_run(C, s, start, len, cnt, base, pos, tag, tok_slot - start, r_st + b * NST);
+      assign_run(C, s, start, len, cnt, base, s_bump, pos, tag, tok_slot - start, r_st + b * NST);
     }
     __syncthreads();
     // append + evict: warp 0 then takes the sequence down to its budget (its
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     const uint32_t old = atomicAdd(arrive, 1u);
     if (old == gridDim.x - 1) {
 #pragma unroll
-      for (int c = 0; c < 3; ++c) C.page_bump[c] = s_bump[c] + s_total[c];
+      for (int c = 0; c < 3; ++c) take_pages(C, c, s_bump[c], s_released[c], s_total[c]);
       *arrive = 0u;
     }
   }

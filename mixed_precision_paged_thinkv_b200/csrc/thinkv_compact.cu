@@ -33,6 +33,7 @@
 
 #include "thinkv_common.cuh"
 #include "thinkv_internal.h"
+#include "thinkv_pages.cuh"
 
 namespace thinkv {
 
@@ -75,10 +76,12 @@ __device__ int block_scan(int v, int* sh, int* total) {
 
 struct CompactWs {
   int32_t* cnt;       // [n][3] live tokens per (call index, class)
-  int32_t* pbase;     // [3][n + 1] first dst page of each call index, per class
+  int32_t* pbase;     // [3][n + 1] first dst page of each call index, per class (virtual
+                      // numbers, thinkv_pages.cuh)
   int32_t* tbase;     // [3][n + 1] first moved-token index, per class (class-major list)
   int32_t* src;       // [max_tokens] source pool slot (page * 16 + slot) of each moved token
-  int32_t* totals;    // [3] pages granted per class; [3]: 1 once the plan succeeded
+  int32_t* totals;    // [3] pages granted per class; [3]: 1 once the plan succeeded;
+                      // [4 + c]: dst's page_bump of class c at the start of the call
 };
 
 constexpr int kScan = 8;     // FIFO entries per lane per pass (loads in flight)
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(kCompactThreads, 1)
       const int pex = block_scan((live + kPage - 1) / kPage, sh, &ptot);
       const int tex = block_scan(live, sh, &ttot);
       if (i < n) {
-        ws.pbase[c * (n + 1) + i] = Dc.page_bump[c] + pcarry + pex;
+        ws.pbase[c * (n + 1) + i] = Dc.page_bump[c] - Dc.page_bump[3 + c] + pcarry + pex;
         ws.tbase[c * (n + 1) + i] = tcarry + tex;
       }
       pcarry += ptot;
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kCompactThreads, 1)
     if (tid == 0) {
       s_tot[c] = pcarry;
       s_ttot[c] = tcarry;
-      ws.pbase[c * (n + 1) + n] = Dc.page_bump[c] + pcarry;
+      ws.pbase[c * (n + 1) + n] = Dc.page_bump[c] - Dc.page_bump[3 + c] + pcarry;
       ws.tbase[c * (n + 1) + n] = tcarry;
     }
   }
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kCompactThreads, 1)
   if (tid == 0) {
     int err = 0;
     for (int c = 0; c < 3; ++c)
-      if ((int64_t)Dc.page_bump[c] + s_tot[c] > Dc.L.pool_pages[c]) err = THINKV_ERR_OUT_OF_PAGES;
+      if (!pool_has(Dc, c, Dc.page_bump[c], Dc.page_bump[3 + c], s_tot[c])) err = THINKV_ERR_OUT_OF_PAGES;
     if ((int64_t)s_ttot[0] + s_ttot[1] + s_ttot[2] > max_tokens) err = THINKV_ERR_INVALID;
     s_err = err;
     if (err) set_status(Dc.status, err);
@@ -197,16 +200,17 @@ __global__ void __launch_bounds__(kCompactThreads, 1)
     for (int c = 0; c < 3; ++c) {
       const int live = ws.cnt[i * 3 + c];
       const int np = (live + kPage - 1) / kPage;
-      const int pb = ws.pbase[c * (n + 1) + i];
+      const int pb = ws.pbase[c * (n + 1) + i], bump = Dc.page_bump[c];
       for (int j = lane; j < np; j += 32) {
+        const int page = granted_page(Dc, c, pb + j, bump);
         const int used = min(kPage, live - j * kPage);
         const uint32_t mask = used >= kPage ? 0xFFFFu : ((1u << used) - 1u);
         const int e = entry0 + j;
-        dtab[e] = make_entry((uint32_t)(pb + j), c, mask);
-        dll[e] = make_live_desc((uint32_t)(pb + j), c, e);
+        dtab[e] = make_entry((uint32_t)page, c, mask);
+        dll[e] = make_live_desc((uint32_t)page, c, e);
         dli[e] = e;
         if (j == np - 1)
-          for (int sl = used; sl < kPage; ++sl) Dc.slot_pos[c][(int64_t)(pb + j) * kPage + sl] = -1;
+          for (int sl = used; sl < kPage; ++sl) Dc.slot_pos[c][(int64_t)page * kPage + sl] = -1;
       }
       const int used_last = live - (np - 1) * kPage;
       const int nfree = np > 0 ? kPage - used_last : 0;
@@ -230,7 +234,8 @@ __global__ void __launch_bounds__(kCompactThreads, 1)
   if (tid == 0) {
     for (int c = 0; c < 3; ++c) {
       ws.totals[c] = s_tot[c];
-      Dc.page_bump[c] += s_tot[c];
+      ws.totals[4 + c] = Dc.page_bump[c];
+      take_pages(Dc, c, Dc.page_bump[c], Dc.page_bump[3 + c], s_tot[c]);
     }
     ws.totals[3] = 1;
   }
@@ -253,7 +258,7 @@ __global__ void compact_list_kernel(CacheView S, CacheView Dc, int32_t n,
     const uint64_t* stab = S.block_table + (int64_t)s * nb_max;
     int entry0 = 0;                               // pages of the earlier classes of s
     for (int c2 = 0; c2 < c; ++c2) entry0 += (ws.cnt[i * 3 + c2] + kPage - 1) / kPage;
-    const int pb = ws.pbase[c * (n + 1) + i];
+    const int pb = ws.pbase[c * (n + 1) + i], bump = ws.totals[4 + c];
     int toff = ws.tbase[c * (n + 1) + i];
     for (int c2 = 0; c2 < c; ++c2) toff += ws.tbase[c2 * (n + 1) + n];
     const int h = S.fifo_head[s * 3 + c], t = S.fifo_tail[s * 3 + c];
@@ -277,7 +282,8 @@ __global__ void compact_list_kernel(CacheView S, CacheView Dc, int32_t n,
 #pragma unroll
       for (int j = 0; j < kScan; ++j) {
         if (e[j] < 0) continue;
-        const int page = pb + kk / kPage, slot = kk % kPage, ent = entry0 + kk / kPage;
+        const int page = granted_page(Dc, c, pb + kk / kPage, bump);
+        const int slot = kk % kPage, ent = entry0 + kk / kPage;
         const int32_t sslot = (int32_t)(entry_page(stab[e[j] >> 4]) * kPage + (e[j] & 15));
         ws.src[toff + kk] = sslot;
         Dc.slot_pos[c][(int64_t)page * kPage + slot] = S.slot_pos[c][sslot];
@@ -440,15 +446,16 @@ __global__ void __launch_bounds__(kCopyWarps * 32, kCopyBlocks)
     const int b = S.L.bits[c];
     const int phb = (int)page_head_bytes(D, G, b);
     const int32_t* pb = ws.pbase + c * (n + 1);
-    const int page = pb[0] + gp;
-    int lo = 0, hi = n;                             // last i with pb[i] <= page
+    const int vpage = pb[0] + gp;
+    int lo = 0, hi = n;                             // last i with pb[i] <= vpage
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pb[mid] <= page) lo = mid; else hi = mid;
+      if (pb[mid] <= vpage) lo = mid; else hi = mid;
     }
     const int i = lo;
     const int live = ws.cnt[i * 3 + c];
-    const int j = page - pb[i];
+    const int j = vpage - pb[i];
+    const int page = granted_page(Dc, c, vpage, ws.totals[4 + c]);
     const int used = min(kPage, live - j * kPage);
     int toff = ws.tbase[c * (n + 1) + i] + j * kPage;
     for (int c2 = 0; c2 < c; ++c2) toff += ws.tbase[c2 * (n + 1) + n];

@@ -105,6 +105,14 @@ size_t compact_workspace_bytes(int32_t n, int32_t max_tokens);
 cudaError_t launch_compact(const CacheView& S, const CacheView& Dc, int32_t n, const int32_t* seq,
                            int32_t max_tokens, void* workspace, int num_sms, cudaStream_t stream);
 
+// release and fork; nseg, settled (and seg): TBE state, or null
+size_t turnover_workspace_bytes(const thinkv_layout& L, int32_t n);
+cudaError_t launch_release(const CacheView& C, int32_t n, const int32_t* seq, int32_t* nseg,
+                           int32_t* settled, void* workspace, int num_sms, cudaStream_t stream);
+cudaError_t launch_fork(const CacheView& C, int32_t n, const int32_t* src, const int32_t* dst, int4* seg,
+                        int32_t* nseg, int32_t* settled, void* workspace, int num_sms,
+                        cudaStream_t stream);
+
 // thought classifier (mechanism only)
 cudaError_t launch_classify(int32_t n, int32_t hq, const float* mass, float theta_t, float theta_r,
                             uint8_t* tags, cudaStream_t stream);
