@@ -664,6 +664,8 @@ __device__ inline void page_step(SegState<D, G>& S, const uint8_t* blk, uint32_t
   for (int gr = 0; gr < NG; ++gr) {
     if constexpr (B == 16) {
       s0[gr] = s1[gr] = 1.f;
+      S.z[gr][0] *= a0;                // no zero term of its own, but the earlier pages' moves with the max
+      S.z[gr][1] *= a1;
     } else {
       const uint32_t p0 = vpar[gr * 16 + g], p1 = vpar[gr * 16 + g + 8];
       const float2 sz0 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
