@@ -450,6 +450,33 @@ THINKV_API int thinkv_decode_attention(const thinkv_cache* cache, int32_t n_seqs
                             int32_t topk, float softmax_scale,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* Workspace bytes thinkv_decode_shared needs on the CURRENT device. */
+THINKV_API size_t thinkv_decode_shared_workspace_bytes(const thinkv_layout* L, int32_t n_seqs, int32_t topk);
+
+/* Decode attention for sequences that share prefixes.  For each i < n_seqs and
+ * each q-head: o = softmax(scale * q K^T) V over the live tokens of sequence
+ * prefix[i] (-1: none) and of seq[i] together, as if they were one sequence;
+ * everything else as thinkv_decode_attention.  A prefix is a sequence of the
+ * same cache (a prompt that was appended once): any sequence may be one,
+ * several rows may name it, seq[i] need not differ from row to row, and a row
+ * that names the same sequence twice counts its tokens twice.
+ * Neighbouring rows with the same prefix[i] form a run, whose prefix is read
+ * once for all of its rows; keep such rows next to each other.  (Rows with the
+ * same prefix apart from each other are right as well, but read it again.)
+ * prefix: device int32 [n_seqs].  A seq[i] or prefix[i] out of range -> *status
+ * = INVALID, and that row decodes as empty.
+ * topk_mass, topk: as thinkv_decode_attention, over both token lists; with it,
+ * every row reads its prefix itself.
+ * workspace: device, >= thinkv_decode_shared_workspace_bytes(L, n_seqs, topk)
+ * bytes, no initialisation needed; calls that share it must not overlap on the
+ * GPU.  Four kernels: the plan (one CTA), the prefix kernel (none of its CTAs
+ * has work when no run is worth it; not launched for one row or with
+ * topk_mass), then decode's split and combine.  1 <= n_seqs <= 16384. */
+THINKV_API int thinkv_decode_shared(const thinkv_cache* cache, int32_t n_seqs, const int32_t* seq,
+                                    const int32_t* prefix, const uint16_t* q, uint16_t* out,
+                                    float* topk_mass, int32_t topk, float softmax_scale,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the library-owned scratch of thinkv_decode_attention_noalloc. */
 #define THINKV_NOALLOC_SCRATCH_BYTES (16u << 20)
 

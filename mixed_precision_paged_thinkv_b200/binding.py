@@ -39,6 +39,7 @@ EXPORTED = [
     "thinkv_evict_slots_workspace_bytes", "thinkv_evict_slots",
     "thinkv_compact_workspace_bytes", "thinkv_compact",
     "thinkv_turnover_workspace_bytes", "thinkv_release", "thinkv_fork",
+    "thinkv_decode_shared_workspace_bytes", "thinkv_decode_shared",
 ]
 
 TBE_BUFFERS = ["seg", "nseg", "settled"]
@@ -131,6 +132,11 @@ def lib():
                                          P, SZ, P]
             L.thinkv_compact.restype = C.c_int
             L.thinkv_classify_thoughts.restype = C.c_int
+            L.thinkv_decode_shared_workspace_bytes.argtypes = [C.POINTER(Layout), I32, I32]
+            L.thinkv_decode_shared_workspace_bytes.restype = SZ
+            L.thinkv_decode_shared.argtypes = [C.POINTER(CacheStruct), I32, P, P, P, P, P, I32,
+                                               C.c_float, P, SZ, P]
+            L.thinkv_decode_shared.restype = C.c_int
             L.thinkv_turnover_workspace_bytes.argtypes = [C.POINTER(Layout), I32]
             L.thinkv_turnover_workspace_bytes.restype = SZ
             L.thinkv_release.argtypes = [C.POINTER(CacheStruct), C.POINTER(TbeStruct), I32, P, P, SZ, P]
@@ -419,6 +425,39 @@ class ThinKVCache:
                                              _ptr(mass) if topk else None, int(topk or 0),
                                              float(softmax_scale), _ptr(ws), ws.numel(),
                                              _stream(stream)), "decode")
+        return out, (mass if topk else None)
+
+    def decode_shared_workspace_bytes(self, n: int, topk: int = 0) -> int:
+        with self._guard():
+            return int(lib().thinkv_decode_shared_workspace_bytes(C.byref(self.layout), n, topk))
+
+    def decode_shared(self, seq: torch.Tensor, prefix: torch.Tensor, q: torch.Tensor,
+                      topk: Optional[int] = None, softmax_scale: float = 0.0,
+                      out: Optional[torch.Tensor] = None, mass: Optional[torch.Tensor] = None, stream=None):
+        """Decode attention over the tokens of prefix[i] (-1: none) and of seq[i]
+        together; neighbouring rows with the same prefix read it once."""
+        n, topk = int(seq.numel()), int(topk or 0)
+        self._expect(seq, torch.int32, n)
+        self._expect(prefix, torch.int32, n)
+        self._expect(q, torch.float16, n * self.Hq * self.d)
+        if out is not None:
+            self._expect(out, torch.float16, n * self.Hq * self.d)
+        if topk and mass is not None:
+            self._expect(mass, torch.float32, n * self.Hq)
+        with self._guard():
+            st = self._stream_here(stream)
+            nbytes = self.decode_shared_workspace_bytes(n, topk)
+            if nbytes == 0:
+                raise ThinkvError(ERR_INVALID, "decode_shared workspace size")
+            with torch.cuda.stream(st):
+                if out is None:
+                    out = torch.empty(n, self.Hq, self.d, dtype=torch.float16, device=q.device)
+                if topk and mass is None:
+                    mass = torch.empty(n, self.Hq, dtype=torch.float32, device=q.device)
+                ws = self._workspace("decode_shared", nbytes)
+            _check(lib().thinkv_decode_shared(C.byref(self.cs), n, _ptr(seq), _ptr(prefix), _ptr(q), _ptr(out),
+                                              _ptr(mass) if topk else None, topk, float(softmax_scale),
+                                              _ptr(ws), ws.numel(), st.cuda_stream), "decode_shared")
         return out, (mass if topk else None)
 
     def status(self, stream=None) -> int:

@@ -16,8 +16,10 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libthinkv.so")
 SOURCES = ["thinkv_api.cu", "thinkv_append.cu", "thinkv_evict.cu", "thinkv_decode.cu",
            "thinkv_noalloc.cu", "thinkv_classify.cu", "thinkv_tbe.cu",
-           "thinkv_compact.cu", "thinkv_victims.cu", "thinkv_turnover.cu"]
-HEADERS = ["thinkv_common.cuh", "thinkv_internal.h", "thinkv_evict_seq.cuh", "thinkv_pages.cuh"]
+           "thinkv_compact.cu", "thinkv_victims.cu", "thinkv_turnover.cu",
+           "thinkv_shared.cu", "thinkv_prefix.cu"]
+HEADERS = ["thinkv_common.cuh", "thinkv_internal.h", "thinkv_evict_seq.cuh", "thinkv_pages.cuh",
+           "thinkv_shared.h"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
@@ -48,7 +50,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return LIB
     out_dir = os.path.join(PKG, "_build")
     os.makedirs(out_dir, exist_ok=True)
-    objs = []
+    objs, jobs = [], []
     flags = NVCC_FLAGS + ["-I", INCLUDE, "-I", CSRC]
     if ptxas_verbose:
         flags = flags + ["-Xptxas", "-v"]
@@ -57,8 +59,12 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         cmd = [nvcc()] + flags + ["-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+        jobs.append((cmd, subprocess.Popen(cmd)))      # the sources compile side by side
         objs.append(obj)
+    codes = [job.wait() for _, job in jobs]
+    for (cmd, _), code in zip(jobs, codes):
+        if code != 0:
+            raise subprocess.CalledProcessError(code, cmd)
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp] + objs + ["-lcudart"]
     if verbose:

@@ -405,6 +405,37 @@ int thinkv_decode_attention(const thinkv_cache* C, int32_t n, const int32_t* seq
                                    softmax_scale, workspace, dl, static_cast<cudaStream_t>(stream)));
 }
 
+size_t thinkv_decode_shared_workspace_bytes(const thinkv_layout* L, int32_t n_seqs, int32_t topk) {
+  if (!layout_ok(L) || n_seqs < 1 || n_seqs > 16384 || topk < 0 || topk > 64) return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const int sms = num_sms_current();
+  DecodeLaunch dl;
+  if (sms <= 0 || !plan_decode_launch(*L, n_seqs, topk, dev, &dl)) return 0;
+  return decode_shared_workspace_bytes(*L, n_seqs, topk, sms, dl);
+}
+
+int thinkv_decode_shared(const thinkv_cache* C, int32_t n, const int32_t* seq, const int32_t* prefix,
+                         const uint16_t* q, uint16_t* out, float* topk_mass, int32_t topk,
+                         float softmax_scale, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cache_ok(C) || n < 1 || n > 16384) return THINKV_ERR_INVALID;
+  if (!seq || !prefix || !q || !out) return THINKV_ERR_INVALID;
+  if (topk_mass && (topk < 1 || topk > 64)) return THINKV_ERR_INVALID;
+  if (!decode_args_aligned(seq, q, out, topk_mass) || !aligned(prefix, 4)) return THINKV_ERR_INVALID;
+  if (workspace && !aligned(workspace, 16)) return THINKV_ERR_INVALID;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return THINKV_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return THINKV_ERR_CUDA;
+  const int k = topk_mass ? topk : 0;
+  DecodeLaunch dl;
+  if (!plan_decode_launch(C->L, n, k, dev, &dl)) return THINKV_ERR_INVALID;
+  if (!workspace || workspace_bytes < decode_shared_workspace_bytes(C->L, n, k, sms, dl))
+    return THINKV_ERR_WORKSPACE;
+  return cuda_status(launch_decode_shared(view_of(C), n, seq, prefix, q, out, topk_mass, k, softmax_scale,
+                                          workspace, sms, dl, static_cast<cudaStream_t>(stream)));
+}
+
 int thinkv_classify_thoughts(int32_t n, int32_t num_q_heads, const float* mass, float theta_t,
                              float theta_r, uint8_t* tags, void* stream) {
   if (n < 0 || num_q_heads < 1) return THINKV_ERR_INVALID;

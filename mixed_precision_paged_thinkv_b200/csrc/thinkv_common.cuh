@@ -197,6 +197,26 @@ __device__ inline uint32_t hsub2_bits(uint32_t a, uint32_t b) {
   return *reinterpret_cast<uint32_t*>(&r);
 }
 
+// Words [w0, w0 + NW) of this lane's portion of a code region laid out in
+// chunks of U = min(16, LB) bytes interleaved over the 32 lanes (see
+// lane_off); `base` is the region + lane * U.  w0 and NW are multiples of U/4,
+// so every load is one whole chunk: 32 lanes read one contiguous span.
+template <int LB, int NW>
+__device__ __forceinline__ void lane_words(const uint8_t* base, int w0, uint32_t (&dst)[NW]) {
+  constexpr int U = LB < 16 ? LB : 16;
+#pragma unroll
+  for (int x = 0; x < NW; x += U / 4) {
+    const uint8_t* ptr = base + ((w0 + x) * 4 / U) * 32 * U;
+    if constexpr (U == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(ptr);
+      dst[x] = v.x; dst[x + 1] = v.y; dst[x + 2] = v.z; dst[x + 3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(ptr);
+      dst[x] = v.x; dst[x + 1] = v.y;
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // code unpacking: element k of the low and of the high half-word of `w`
 // (b-bit codes, element k at bits [b*k, b*k+b) of its half) as the half2

@@ -33,8 +33,11 @@
 #include <mutex>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "thinkv_common.cuh"
 #include "thinkv_internal.h"
+#include "thinkv_shared.h"
 
 namespace thinkv {
 
@@ -83,7 +86,18 @@ struct DecodeParams {
   int32_t* status;
   int32_t nstage, stage_bytes, warp_smem, plan_smem;
   int32_t q_off, q_bytes;  // Q rows of a segment ride with its first page: stage + q_off
+  // shared-prefix decode (the kernels' SHARED form): the plan, and the partial
+  // rows the prefix kernel's CTAs left
+  SharedPlan plan;
+  const float* prefix_o;
+  const float2* prefix_ml;
+  int32_t prefix_grid;
 };
+
+// Prefix sums of live pages over the call: 64-bit in the SHARED form, where a
+// prefix read by many sequences counts once for each.
+template <bool SHARED>
+using pages_t = std::conditional_t<SHARED, int64_t, int32_t>;
 
 __device__ inline float pow2i(int e) { return __int_as_float((127 + e) << 23); }
 
@@ -303,12 +317,14 @@ __device__ inline void bitonic128_merge_desc(float (&v)[4]) {
 }
 
 // Sequences with no live token: zeros (and mass 0), written by the grid.
-__device__ void write_empty_outputs(const DecodeParams& p, const int32_t* P, int D) {
+template <bool SHARED>
+__device__ void write_empty_outputs(const DecodeParams& p, const pages_t<SHARED>* P, int D) {
   const int64_t nthreads = (int64_t)gridDim.x * blockDim.x;
   const int64_t tid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   for (int64_t x = tid; x < (int64_t)p.n * p.Hq; x += nthreads) {
     const int i = (int)(x / p.Hq);
     if (P[i + 1] != P[i]) continue;
+    if (SHARED && p.plan.item[i].w >= 0) continue;   // the prefix kernel has its tokens
     uint16_t* o = p.out + x * D;
     for (int c = 0; c < D; ++c) o[c] = 0;
     if (p.mass) p.mass[x] = 0.f;
@@ -371,9 +387,9 @@ __device__ inline void seg_begin(SegState<D, G>& S, const DecodeParams& p, const
 }
 
 // Unit range [Us, Ue) of segment (i, h) in the call's list of live page-heads.
-__device__ inline void seg_range(const DecodeParams& p, const int32_t* P, int i, int h,
-                                 int64_t* Us, int64_t* Ue) {
-  const int nl = P[i + 1] - P[i];
+template <typename T>
+__device__ inline void seg_range(const DecodeParams& p, const T* P, int i, int h, int64_t* Us, int64_t* Ue) {
+  const int nl = (int)(P[i + 1] - P[i]);
   *Us = (int64_t)P[i] * p.Hkv + (int64_t)h * nl;
   *Ue = *Us + nl;
 }
@@ -384,11 +400,22 @@ __device__ inline int64_t warp_of_unit(int64_t u, int64_t T, int64_t W) {
   return ((u + 1) * W - 1) / T;
 }
 
+// Live tokens that row i attends over.
+template <bool SHARED>
+__device__ inline pages_t<SHARED> live_tokens(const DecodeParams& p, int i) {
+  if constexpr (SHARED) {
+    const int4 it = p.plan.item[i];
+    return (it.x >= 0 ? (int64_t)p.live_count[it.x] : 0) + (it.y >= 0 ? (int64_t)p.live_count[it.y] : 0);
+  } else {
+    return p.live_count[p.seq[i]];
+  }
+}
+
 // Ends the warp's work on segment seg = i * Hkv + h.  If the whole segment
 // was in this warp (Us >= U0 and Ue <= U1) its O rows and top-k mass are
 // written at once; otherwise the warp's piece record goes to rec[w + seg]
 // for the merge.
-template <int D, int G, bool TOPK>
+template <int D, int G, bool TOPK, bool SHARED>
 __device__ inline void seg_end(SegState<D, G>& S, const DecodeParams& p, int64_t w, int seg,
                                const TopkCtx& tk, bool whole) {
   constexpr int NG = SegState<D, G>::NG, MT = SegState<D, G>::MT;
@@ -449,7 +476,7 @@ __device__ inline void seg_end(SegState<D, G>& S, const DecodeParams& p, int64_t
         *reinterpret_cast<float4*>(tl + hd * kCandCap + 4 * lane) = v;
       }
     } else {
-      const bool all = p.live_count[p.seq[i]] <= tk.topk;
+      const bool all = live_tokens<SHARED>(p, i) <= tk.topk;
       for (int hd = 0; hd < Gq; ++hd) {
         float sum = 0.f;
         if (!all) {
@@ -476,26 +503,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-
-// Words [w0, w0 + NW) of this lane's portion of a code region laid out in
-// chunks of U = min(16, LB) bytes interleaved over the 32 lanes (see
-// lane_off); `base` is the region + lane * U.  w0 and NW are multiples of U/4,
-// so every load is one whole chunk: 32 lanes read one contiguous span.
-template <int LB, int NW>
-__device__ __forceinline__ void lane_words(const uint8_t* base, int w0, uint32_t (&dst)[NW]) {
-  constexpr int U = LB < 16 ? LB : 16;
-#pragma unroll
-  for (int x = 0; x < NW; x += U / 4) {
-    const uint8_t* ptr = base + ((w0 + x) * 4 / U) * 32 * U;
-    if constexpr (U == 16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(ptr);
-      dst[x] = v.x; dst[x + 1] = v.y; dst[x + 2] = v.z; dst[x + 3] = v.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(ptr);
-      dst[x] = v.x; dst[x + 1] = v.y;
-    }
-  }
 }
 
 // One live page-head block (in shared memory) of a class with B-bit codes.
@@ -838,7 +845,8 @@ struct UnitMeta {
   uint32_t mask;
 };
 
-__device__ inline UnitMeta resolve_unit(const DecodeParams& p, const int32_t* P, int64_t u,
+template <bool SHARED>
+__device__ inline UnitMeta resolve_unit(const DecodeParams& p, const pages_t<SHARED>* P, int64_t u,
                                         int64_t U1) {
   UnitMeta m;
   m.src_lo = m.src_hi = 0;
@@ -851,10 +859,19 @@ __device__ inline UnitMeta resolve_unit(const DecodeParams& p, const int32_t* P,
     if ((int64_t)P[mid] * p.Hkv <= u) lo = mid; else hi = mid;
   }
   const int i = lo;
-  const int nl = P[i + 1] - P[i];
-  const int rel = (int)(u - (int64_t)P[i] * p.Hkv);   // < Hkv * max_blocks_per_seq < 2^31
-  const int h = rel / nl, j = rel - h * nl;
-  const int64_t row = (int64_t)P[p.n + 1 + i] * p.max_blocks;   // the sequence id, cached
+  const int nl = (int)(P[i + 1] - P[i]);
+  const int rel = (int)(u - (int64_t)P[i] * p.Hkv);   // < Hkv * 2 max_blocks_per_seq <= 2^30
+  const int h = rel / nl;
+  int j = rel - h * nl;
+  int64_t row;
+  if constexpr (SHARED) {
+    // the prefix's pages first, where this sequence reads them itself
+    const int4 it = p.plan.item[i];
+    row = (int64_t)(j < it.z ? it.y : it.x) * p.max_blocks;
+    j -= j < it.z ? 0 : it.z;
+  } else {
+    row = (int64_t)P[p.n + 1 + i] * p.max_blocks;     // the sequence id, cached
+  }
   const uint64_t desc = p.live_list[row + j];       // page | class << 32 | entry << 40
   const int cls = entry_class(desc);
   const uint64_t src = reinterpret_cast<uint64_t>(p.pool[cls]) +
@@ -866,23 +883,27 @@ __device__ inline UnitMeta resolve_unit(const DecodeParams& p, const int32_t* P,
   return m;
 }
 
-template <int D, int G, bool TOPK>
+template <int D, int G, bool TOPK, bool SHARED>
 __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
     decode_split_kernel(DecodeParams p) {
   constexpr int kDecWarps = SplitShape<D>::warps, kDecThreads = SplitShape<D>::threads;
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int32_t* P = reinterpret_cast<int32_t*>(smem);      // [n + 1] prefix of live pages
-  int32_t* Sq = P + (p.n + 1);                         // [n] the call's sequence ids
+  pages_t<SHARED>* P = reinterpret_cast<pages_t<SHARED>*>(smem);   // [n + 1] prefix of live pages
   pdl_launch_dependents();
-  // the call's own inputs may be read before the previous kernel has finished
-  for (int i = tid; i < p.n; i += kDecThreads) Sq[i] = p.seq[i];
-  // everything below reads cache state: wait for the previous kernel
-  pdl_wait();
-  __syncthreads();
+  if constexpr (SHARED) {
+    pdl_wait();
+    for (int i = tid; i <= p.n; i += kDecThreads) P[i] = p.plan.pref[i];   // the plan's
+    __syncthreads();
+  } else {
+    int32_t* Sq = P + (p.n + 1);                       // [n] the call's sequence ids
+    // the call's own inputs may be read before the previous kernel has finished
+    for (int i = tid; i < p.n; i += kDecThreads) Sq[i] = p.seq[i];
+    // everything below reads cache state: wait for the previous kernel
+    pdl_wait();
+    __syncthreads();
 
-  // ---- prefix of live pages over the call's sequences (per CTA) ----
-  {
+    // ---- prefix of live pages over the call's sequences (per CTA) ----
     __shared__ int wsum[kDecWarps];
     int carry = 0;
     for (int base = 0; base < p.n; base += kDecThreads) {
@@ -911,10 +932,10 @@ __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
     }
     if (tid == 0) P[p.n] = carry;
     __syncthreads();
+    if (blockIdx.x == 0)
+      for (int x = tid; x <= p.n; x += kDecThreads) p.pref[x] = P[x];   // for the combine
   }
-  if (blockIdx.x == 0)
-    for (int x = tid; x <= p.n; x += kDecThreads) p.pref[x] = P[x];   // for the combine
-  write_empty_outputs(p, P, D);
+  write_empty_outputs<SHARED>(p, P, D);
 
   const int64_t T = (int64_t)P[p.n] * p.Hkv;
   const int64_t W = (int64_t)gridDim.x * kDecWarps;
@@ -939,8 +960,8 @@ __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
   }
   __syncwarp();
 
-  UnitMeta cur = resolve_unit(p, P, U0 + lane, U1);
-  UnitMeta nxt = resolve_unit(p, P, U0 + 32 + lane, U1);
+  UnitMeta cur = resolve_unit<SHARED>(p, P, U0 + lane, U1);
+  UnitMeta nxt = resolve_unit<SHARED>(p, P, U0 + 32 + lane, U1);
   const int nu = (int)(U1 - U0);   // units of one warp: < 2^31
 
   // Issues unit ku (its lane in `m`) into stage st: the page-head block, plus
@@ -967,6 +988,9 @@ __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
     }
   };
 
+  // whether row i's tokens are all in this kernel's list
+  auto alone = [&](int i) { return !SHARED || p.plan.item[i].w < 0; };
+
   // only the first page goes out before the loop: copies issued together all
   // land together, so the rest of the ring is filled once the first has landed
   issue(cur, 0, 0);
@@ -980,7 +1004,7 @@ __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
     const int kk = k & 31;
     if (kk == 0 && k > 0) {
       cur = nxt;
-      nxt = resolve_unit(p, P, U0 + k + 32 + lane, U1);
+      nxt = resolve_unit<SHARED>(p, P, U0 + k + 32 + lane, U1);
     }
     if (!mbar_wait_bounded(&bars[stage], parity)) {
       if (lane == 0) set_status(p.status, THINKV_ERR_TIMEOUT);
@@ -1000,7 +1024,7 @@ __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
       if (seg >= 0) {
         int64_t Us, Ue;
         seg_range(p, P, seg / p.Hkv, seg % p.Hkv, &Us, &Ue);
-        seg_end<D, G, TOPK>(S, p, w, seg, tk, Us >= U0 && Ue <= U1);
+        seg_end<D, G, TOPK, SHARED>(S, p, w, seg, tk, Us >= U0 && Ue <= U1 && alone(seg / p.Hkv));
       }
       seg = useg;
       seg_begin<D, G>(S, p, reinterpret_cast<const uint16_t*>(blk + p.q_off),
@@ -1022,7 +1046,7 @@ __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
   {
     int64_t Us, Ue;
     seg_range(p, P, seg / p.Hkv, seg % p.Hkv, &Us, &Ue);
-    seg_end<D, G, TOPK>(S, p, w, seg, tk, Us >= U0 && Ue <= U1);
+    seg_end<D, G, TOPK, SHARED>(S, p, w, seg, tk, Us >= U0 && Ue <= U1 && alone(seg / p.Hkv));
   }
 }
 
@@ -1039,7 +1063,37 @@ constexpr int kCombinePieces = 128;             // pieces per round of the weigh
 // piece's top-k candidates for head r and merges their largest into a running
 // list (bitonic networks, the next piece's candidates loaded while the current
 // ones are sorted) for the top-k mass.
-template <int D, bool TOPK>
+// A row's pieces from the prefix kernel: the CTAs of its grid that hold units of
+// the row's segment, two partials each where the block has at most 128 rows.
+struct PrefixPieces {
+  int64_t units, first_unit, first_cta, base;
+  int count, halves, half_rows;
+  bool by_unit;
+  __device__ void find(const DecodeParams& p, int i, int h, int r) {
+    const SharedRun run = p.plan.run[r];
+    const RunShape s = run_shape(run.count, run.pages, p.Gq);
+    const int b = (i - run.first) / s.members, in_block = (i - run.first) - b * s.members;
+    half_rows = min(s.members, run.count - b * s.members) * p.Gq;
+    halves = half_rows > 128 ? 1 : 2;
+    units = p.plan.rstart[*p.plan.nruns];
+    first_unit = p.plan.rstart[r] + ((int64_t)h * s.blocks + b) * s.tiles;
+    by_unit = units <= p.prefix_grid;
+    first_cta = warp_of_unit(first_unit, units, p.prefix_grid);
+    const int64_t last = warp_of_unit(first_unit + s.tiles - 1, units, p.prefix_grid);
+    count = halves * (int)(by_unit ? s.tiles : last - first_cta + 1);
+    base = partial_row(run, s, p.Hkv, p.Gq, h, b, 0) + (int64_t)in_block * p.Gq;
+  }
+  // row of piece x for the first of the kv-head's query heads
+  __device__ int64_t row(const DecodeParams& p, int x) const {
+    const int j = halves == 2 ? x >> 1 : x;
+    const int64_t c = by_unit ? warp_of_unit(first_unit + j, units, p.prefix_grid) : first_cta + j;
+    return base + c * kBlockRows + (halves == 2 && (x & 1) ? half_rows : 0);
+  }
+};
+
+// SHARED: the partial rows that the prefix kernel left for the row follow the
+// split kernel's records in the list of pieces.
+template <int D, bool TOPK, bool SHARED>
 __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_kernel(DecodeParams p) {
   constexpr int QD = D / 4;
   __shared__ float sM[8], sL[8];
@@ -1049,17 +1103,33 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   pdl_wait();                                   // records and prefix come from the split kernel
   const int seg = blockIdx.x;
   const int i = seg / p.Hkv, h = seg - (seg / p.Hkv) * p.Hkv;
-  const int nl = p.pref[i + 1] - p.pref[i];
-  if (nl == 0) return;                          // written by the split kernel
-  const int64_t T = (int64_t)p.pref[p.n] * p.Hkv, W = p.split_warps;
-  const int64_t Us = (int64_t)p.pref[i] * p.Hkv + (int64_t)h * nl, Ue = Us + nl;
-  const int64_t w0 = warp_of_unit(Us, T, W), w1 = warp_of_unit(Ue - 1, T, W);
+  const pages_t<SHARED>* pref;
+  if constexpr (SHARED) pref = p.plan.pref;
+  else pref = p.pref;
+  const int nl = (int)(pref[i + 1] - pref[i]);
+  if (!SHARED && nl == 0) return;               // written by the split kernel
+  const int64_t T = (int64_t)pref[p.n] * p.Hkv, W = p.split_warps;
+  const int64_t Us = (int64_t)pref[i] * p.Hkv + (int64_t)h * nl, Ue = Us + nl;
+  const bool any = !SHARED || nl > 0;
+  const int64_t w0 = any ? warp_of_unit(Us, T, W) : 0, w1 = any ? warp_of_unit(Ue - 1, T, W) : 0;
   const bool by_unit = T <= W;                  // one unit per warp
-  const int np = (int)(by_unit ? nl : w1 - w0 + 1);
-  if (np <= 1) return;                          // finished inside one split warp
+  const int np_split = any ? (int)(by_unit ? nl : w1 - w0 + 1) : 0;
+  int np = np_split;
+  PrefixPieces pp;                              // of the prefix kernel (SHARED)
+  if constexpr (SHARED) {
+    const int r = p.plan.item[i].w;
+    if (r >= 0) {
+      pp.find(p, i, h, r);
+      np += pp.count;
+    } else if (np <= 1) {
+      return;
+    }
+  } else {
+    if (np <= 1) return;                        // finished inside one split warp
+  }
   const int Gq = p.Gq, k = p.topk;
   // the top-k warps' live count, requested now and used after the merge
-  const int live_i = (p.mass && threadIdx.x < 32 * Gq) ? p.live_count[p.seq[i]] : 0;
+  const pages_t<SHARED> live_i = (p.mass && threadIdx.x < 32 * Gq) ? live_tokens<SHARED>(p, i) : 0;
   const int64_t rb = record_bytes(Gq, D, k);
   const uint8_t* recs = reinterpret_cast<const uint8_t*>(p.rec);
   auto rec = [&](int j) -> const uint8_t* {
@@ -1082,10 +1152,13 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   const int r_o = tid / QD, q_o = tid - (tid / QD) * QD;
   const bool out_thread = tid < Gq * QD;
   auto quad = [&](int j) {
+    if (SHARED && j >= np_split)
+      return __ldcg(reinterpret_cast<const float4*>(p.prefix_o + (pp.row(p, j - np_split) + r_o) * D) + q_o);
     return __ldcg(reinterpret_cast<const float4*>(rec(j) + 64) + r_o * QD + q_o);
   };
   auto pair_ml = [&](int x) {
     const int j = x / Gq, r = x - j * Gq;
+    if (SHARED && j >= np_split) return __ldcg(p.prefix_ml + pp.row(p, j - np_split) + r);
     return __ldcg(reinterpret_cast<const float2*>(rec(j)) + r);
   };
   // the first pieces' quads and (m, l) pairs do not depend on the weights:
@@ -1293,7 +1366,7 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   if (lane == 0) p.mass[mrow] = sum / sL[r];
 }
 
-template <int D, int G, bool TOPK>
+template <int D, int G, bool TOPK, bool SHARED>
 cudaError_t launch_split_t(const DecodeParams& p, const DecodeLaunch& dl, cudaStream_t stream) {
   // raise the dynamic shared-memory limit of this instantiation once per
   // device (and again whenever a launch needs more); host threads that decode
@@ -1308,13 +1381,13 @@ cudaError_t launch_split_t(const DecodeParams& p, const DecodeLaunch& dl, cudaSt
   {
     std::lock_guard<std::mutex> guard(lock);
     if (dl.smem_bytes > configured[dev]) {
-      e = cudaFuncSetAttribute(decode_split_kernel<D, G, TOPK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      e = cudaFuncSetAttribute(decode_split_kernel<D, G, TOPK, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)dl.smem_bytes);
       if (e != cudaSuccess) return e;
       configured[dev] = dl.smem_bytes;
     }
   }
-  e = launch_pdl(decode_split_kernel<D, G, TOPK>, dim3(dl.grid), dim3(SplitShape<D>::threads), dl.smem_bytes,
+  e = launch_pdl(decode_split_kernel<D, G, TOPK, SHARED>, dim3(dl.grid), dim3(SplitShape<D>::threads), dl.smem_bytes,
                  stream, p);
   if (e != cudaSuccess) return e;
   // the combine: one CTA per segment (most return at once), as many threads as
@@ -1322,14 +1395,18 @@ cudaError_t launch_split_t(const DecodeParams& p, const DecodeLaunch& dl, cudaSt
   // per-head sums, the top-k merges)
   const int qt = (p.Gq * (D / 4) + 31) / 32 * 32;
   const int ct = qt > 32 * p.Gq ? qt : 32 * p.Gq;
-  return launch_pdl(decode_combine_kernel<D, TOPK>, dim3((unsigned)(p.n * p.Hkv)),
+  return launch_pdl(decode_combine_kernel<D, TOPK, SHARED>, dim3((unsigned)(p.n * p.Hkv)),
                     dim3(ct < kCombineThreads ? ct : kCombineThreads), 0, stream, p);
 }
 
 // the top-k candidate code is compiled only into the instantiation that uses it
 template <int D, int G>
-cudaError_t launch_split(const DecodeParams& p, const DecodeLaunch& dl, cudaStream_t stream) {
-  return p.topk > 0 ? launch_split_t<D, G, true>(p, dl, stream) : launch_split_t<D, G, false>(p, dl, stream);
+cudaError_t launch_split(const DecodeParams& p, bool shared, const DecodeLaunch& dl, cudaStream_t stream) {
+  if (shared)
+    return p.topk > 0 ? launch_split_t<D, G, true, true>(p, dl, stream)
+                      : launch_split_t<D, G, false, true>(p, dl, stream);
+  return p.topk > 0 ? launch_split_t<D, G, true, false>(p, dl, stream)
+                    : launch_split_t<D, G, false, false>(p, dl, stream);
 }
 
 int plan_smem_bytes(int32_t n) { return ((2 * n + 1) * 4 + 127) / 128 * 128; }
@@ -1404,12 +1481,14 @@ size_t decode_workspace_bytes(const thinkv_layout& L, int32_t n_seqs, int32_t to
   return b;
 }
 
-cudaError_t launch_decode(const CacheView& C, int32_t n, const int32_t* seq, const uint16_t* q,
-                          uint16_t* out, float* mass, int32_t topk, float softmax_scale,
-                          void* ws, const DecodeLaunch& dl, cudaStream_t stream) {
+namespace {
+
+// What a decode call's kernels need, but for their workspace.
+DecodeParams decode_params(const CacheView& C, int32_t n, const int32_t* seq, const uint16_t* q, uint16_t* out,
+                           float* mass, int32_t topk, float softmax_scale, const DecodeLaunch& dl) {
   const thinkv_layout& L = C.L;
   const int D = L.head_dim, G = L.group_size;
-  DecodeParams p;
+  DecodeParams p = {};
   for (int c = 0; c < 3; ++c) {
     p.pool[c] = C.pool[c];
     p.phb[c] = (int32_t)page_head_bytes(D, G, L.bits[c]);
@@ -1429,14 +1508,7 @@ cudaError_t launch_decode(const CacheView& C, int32_t n, const int32_t* seq, con
   p.q = q;
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)D);
   p.scale_log2 = scale * 1.4426950408889634f;  // log2(e)
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  p.pref = reinterpret_cast<int32_t*>(w);
-  {
-    const size_t head = (size_t)(n + 1 > n * L.num_kv_heads ? n + 1 : n * L.num_kv_heads);
-    w += (head * 4 + 255) / 256 * 256;
-  }
   p.topk = mass ? topk : 0;
-  p.rec = w;
   p.split_warps = (int64_t)dl.grid * dl.warps_per_cta;
   p.live_count = C.live_count;
   p.out = out;
@@ -1452,12 +1524,107 @@ cudaError_t launch_decode(const CacheView& C, int32_t n, const int32_t* seq, con
     p.q_bytes = p.Gq * D * 2;
   }
   p.plan_smem = plan_smem_bytes(n);
-  cudaError_t e;
-  if (D == 128 && G == 64) e = launch_split<128, 64>(p, dl, stream);
-  else if (D == 128 && G == 32) e = launch_split<128, 32>(p, dl, stream);
-  else if (D == 64 && G == 64) e = launch_split<64, 64>(p, dl, stream);
-  else e = launch_split<64, 32>(p, dl, stream);
-  return e;
+  return p;
+}
+
+cudaError_t launch_kernels(const DecodeParams& p, int D, int G, bool shared, const DecodeLaunch& dl,
+                           cudaStream_t stream) {
+  if (D == 128 && G == 64) return launch_split<128, 64>(p, shared, dl, stream);
+  if (D == 128 && G == 32) return launch_split<128, 32>(p, shared, dl, stream);
+  if (D == 64 && G == 64) return launch_split<64, 64>(p, shared, dl, stream);
+  return launch_split<64, 32>(p, shared, dl, stream);
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+cudaError_t launch_decode(const CacheView& C, int32_t n, const int32_t* seq, const uint16_t* q,
+                          uint16_t* out, float* mass, int32_t topk, float softmax_scale,
+                          void* ws, const DecodeLaunch& dl, cudaStream_t stream) {
+  const thinkv_layout& L = C.L;
+  DecodeParams p = decode_params(C, n, seq, q, out, mass, topk, softmax_scale, dl);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.pref = reinterpret_cast<int32_t*>(w);
+  {
+    const size_t head = (size_t)(n + 1 > n * L.num_kv_heads ? n + 1 : n * L.num_kv_heads);
+    w += (head * 4 + 255) / 256 * 256;
+  }
+  p.rec = w;
+  return launch_kernels(p, L.head_dim, L.group_size, false, dl, stream);
+}
+
+// The prefix kernel takes one CTA per SM; a call with the top-k statistic or of
+// one sequence has no use for it.
+static bool with_prefix_kernel(int32_t n, int32_t topk) { return n > 1 && topk == 0; }
+
+size_t decode_shared_workspace_bytes(const thinkv_layout& L, int32_t n, int32_t topk, int num_sms,
+                                     const DecodeLaunch& dl) {
+  const int Gq = L.num_q_heads / L.num_kv_heads;
+  size_t b = 256 + round256((size_t)n * sizeof(int4)) + round256(((size_t)n + 1) * 8) +
+             round256((size_t)(n / 2 + 1) * sizeof(SharedRun)) + round256((size_t)(n / 2 + 2) * 8) +
+             2 * round256(((size_t)n + 1) * 4);
+  b += round256((size_t)dl.pieces * (size_t)record_bytes(Gq, L.head_dim, topk));
+  if (with_prefix_kernel(n, topk)) {
+    const size_t rows = (size_t)partial_rows(L, n, num_sms);
+    b += round256(rows * sizeof(float2)) + rows * L.head_dim * 4;
+  }
+  return b;
+}
+
+cudaError_t launch_decode_shared(const CacheView& C, int32_t n, const int32_t* seq, const int32_t* prefix,
+                                 const uint16_t* q, uint16_t* out, float* mass, int32_t topk,
+                                 float softmax_scale, void* ws, int num_sms, const DecodeLaunch& dl,
+                                 cudaStream_t stream) {
+  const thinkv_layout& L = C.L;
+  const int D = L.head_dim, G = L.group_size;
+  DecodeParams p = decode_params(C, n, seq, q, out, mass, topk, softmax_scale, dl);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  auto take = [&](size_t bytes) {
+    uint8_t* at = w;
+    w += round256(bytes);
+    return at;
+  };
+  p.plan.nruns = reinterpret_cast<int32_t*>(take(256));
+  p.plan.item = reinterpret_cast<int4*>(take((size_t)n * sizeof(int4)));
+  p.plan.pref = reinterpret_cast<int64_t*>(take(((size_t)n + 1) * 8));
+  p.plan.run = reinterpret_cast<SharedRun*>(take((size_t)(n / 2 + 1) * sizeof(SharedRun)));
+  p.plan.rstart = reinterpret_cast<int64_t*>(take((size_t)(n / 2 + 2) * 8));
+  p.plan.start = reinterpret_cast<int32_t*>(take(((size_t)n + 1) * 4));
+  p.plan.used = reinterpret_cast<int32_t*>(take(((size_t)n + 1) * 4));
+  p.rec = take((size_t)dl.pieces * (size_t)record_bytes(p.Gq, D, p.topk));
+  const bool with_prefix = with_prefix_kernel(n, p.topk);
+  cudaError_t e = launch_shared_plan(C, n, seq, prefix, !with_prefix, p.plan, stream);
+  if (e != cudaSuccess) return e;
+  if (with_prefix) {
+    const size_t rows = (size_t)partial_rows(L, n, num_sms);
+    float2* ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
+    float* o = reinterpret_cast<float*>(w);
+    p.prefix_ml = ml;
+    p.prefix_o = o;
+    p.prefix_grid = num_sms;
+    PrefixParams x = {};
+    for (int c = 0; c < 3; ++c) {
+      x.pool[c] = p.pool[c];
+      x.phb[c] = p.phb[c];
+      x.bits[c] = L.bits[c] + (L.fmt[c] == 1 ? 256 : 0);
+    }
+    x.table = p.table;
+    x.live_list = p.live_list;
+    x.max_blocks = p.max_blocks;
+    x.Hkv = p.Hkv;
+    x.Hq = p.Hq;
+    x.Gq = p.Gq;
+    x.q = q;
+    x.scale_log2 = p.scale_log2;
+    x.plan = p.plan;
+    x.o = o;
+    x.ml = ml;
+    x.status = p.status;
+    e = launch_prefix(x, D, G, num_sms, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kernels(p, D, G, true, dl, stream);
 }
 
 }  // namespace thinkv

@@ -91,6 +91,14 @@ cudaError_t launch_decode(const CacheView& C, int32_t n, const int32_t* seq, con
                           uint16_t* out, float* mass, int32_t topk, float softmax_scale,
                           void* ws, const DecodeLaunch& dl, cudaStream_t stream);
 
+// decode with a prefix shared by several sequences
+size_t decode_shared_workspace_bytes(const thinkv_layout& L, int32_t n_seqs, int32_t topk, int num_sms,
+                                     const DecodeLaunch& dl);
+cudaError_t launch_decode_shared(const CacheView& C, int32_t n, const int32_t* seq, const int32_t* prefix,
+                                 const uint16_t* q, uint16_t* out, float* mass, int32_t topk,
+                                 float softmax_scale, void* ws, int num_sms, const DecodeLaunch& dl,
+                                 cudaStream_t stream);
+
 // TBE (segment-level eviction on Transition thoughts)
 cudaError_t launch_tbe(const CacheView& C, int4* seg, int32_t* nseg, int32_t* settled, int32_t n,
                        const int32_t* seq, const int32_t* pos, const uint8_t* tag, int32_t t_min,

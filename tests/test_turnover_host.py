@@ -102,3 +102,26 @@ def test_model_round_trip():
     assert b["pool_R"][2].tolist() == [0] * 8 and b["slot_pos_R"][3].tolist() == b["slot_pos_R"][1].tolist()
     M.release(b, [2], pool)
     assert b["page_bump"][3:6].tolist() == [2, 1, 0] and b["page_bump"][6:8].tolist() == [3, 2]
+
+
+def test_decode_shared_arguments_are_refused_before_any_launch(lib):
+    cs = _cache()
+    ok, odd, word = C.c_void_p(4096), C.c_void_p(4098), C.c_void_p(4100)
+    f, c, big = lib.thinkv_decode_shared, None, 10 ** 9
+    c = C.byref(cs)
+    for n in (0, -1, 16385):
+        assert f(c, n, ok, ok, ok, ok, None, 0, 0.0, ok, big, None) == 1
+    for hole in range(4):                              # seq, prefix, q, out
+        args = [ok] * 4
+        args[hole] = None
+        assert f(c, 4, *args, None, 0, 0.0, ok, big, None) == 1
+    assert f(c, 4, odd, ok, ok, ok, None, 0, 0.0, ok, big, None) == 1
+    assert f(c, 4, ok, odd, ok, ok, None, 0, 0.0, ok, big, None) == 1
+    assert f(c, 4, ok, ok, word, ok, None, 0, 0.0, ok, big, None) == 1
+    assert f(c, 4, ok, ok, ok, word, None, 0, 0.0, ok, big, None) == 1
+    assert f(c, 4, ok, ok, ok, ok, odd, 4, 0.0, ok, big, None) == 1
+    assert f(c, 4, ok, ok, ok, ok, None, 0, 0.0, word, big, None) == 1
+    for topk in (0, 65):
+        assert f(c, 4, ok, ok, ok, ok, ok, topk, 0.0, ok, big, None) == 1
+    w = lib.thinkv_decode_shared_workspace_bytes
+    assert w(C.byref(cs.L), 0, 0) == 0 and w(C.byref(cs.L), 16385, 0) == 0 and w(C.byref(cs.L), 4, 65) == 0
