@@ -44,8 +44,13 @@ namespace {
 constexpr int kTile = kTilePages * kPage;     // 128 key slots
 constexpr int kDequantWarps = kTilePages;
 constexpr int kWarpMma = 16, kWarpLoad = 17;
-constexpr int kThreads = 18 * 32;
-constexpr int kSlots = 32;                    // raw page slots in flight (4 tiles)
+// Five warpgroups, so that registers can move between them (setmaxnreg): the
+// launch's 640 x 96 become 152 for softmax, 56 for the dequantising warps and 64
+// for the last group.
+constexpr int kThreads = 20 * 32;
+constexpr int kRegsSoftmax = 152, kRegsDequant = 56, kRegsLast = 64;
+static_assert(256 * kRegsSoftmax + 256 * kRegsDequant + 128 * kRegsLast <= kThreads * 96, "register shares");
+constexpr int kSlots = 4;                     // tiles of raw pages in flight
 constexpr float kHeadroom = 7.f;              // P starts at 2^7 at a row's maximum
 constexpr float kSlack = 8.f;                 // and grows by up to 2^8 before a rescale
 
@@ -66,10 +71,9 @@ struct Misc {
   uint64_t raw_full[kSlots], raw_empty[kSlots];
   uint64_t kv_full[6], kv_empty[6];
   uint64_t s_full[2], p_full[2], o_full[2], q_full, drain;
-  uint32_t slot_off[kSlots];                  // where the slot's block lies in the ring
-  uint32_t slot_bits[kSlots];                 // its class's bits (0: no page)
-  uint32_t slot_size[kSlots];                 // ring bytes it holds (loader's books)
-  uint16_t mask[4][kTilePages];               // live masks of the last four tiles
+  uint32_t slot_off[kSlots][kTilePages];      // where each page's block lies in the ring
+  uint32_t slot_bits[kSlots][kTilePages];     // its class's bits | live mask << 16 (0: no page)
+  alignas(16) uint16_t mask[4][kTilePages];   // live masks of the last four tiles
   uint32_t tmem;
   volatile int abort;
 };
@@ -146,21 +150,15 @@ __device__ inline void mbar_arrive(uint64_t* bar) {
   asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0];\n\t}" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Waits for a phase for two seconds at most; false when they ran out or another
-// role gave up.
-constexpr uint64_t kWaitNs = 2000000000ull;
-__device__ inline uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ inline bool wait_role(Misc* m, uint64_t* bar, uint32_t parity) {
-  if (mbar_test_wait(bar, parity)) return true;
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = now_ns();
-  while (!m->abort && now_ns() - t0 < kWaitNs)
-    for (int it = 0; it < 32; ++it)
-      if (mbar_try_wait(bar, parity)) return true;
+// Waits for a phase, with a limit on the probes; false when they ran out or
+// another role gave up.  (A probe with a time hint of its own is compiled to
+// a loop of sleeps, which wakes late.)
+__device__ __forceinline__ bool wait_role(Misc* m, uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t it = 0; it < kWaitLimit; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (m->abort) return false;
+  }
   m->abort = 1;
   return false;
 }
@@ -207,17 +205,19 @@ __device__ inline Piece piece_at(const PrefixParams& p, int nruns, int64_t u, in
 // ---------------------------------------------------------------------------
 // codes -> fp16 operands
 // ---------------------------------------------------------------------------
+__device__ inline __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ inline uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
 template <int B, int F>
 __device__ constexpr float largest_code() {
   return F == 1 ? (B == 8 ? 448.f : B == 4 ? 6.f : 2.f) : (float)((1 << B) - 1);   // (ternary codes: 0..2)
 }
-
-// A scale whose largest value zero + scale * code would round past fp16's
-// range is lowered to what fits (a value past 65504 + 16 would become inf).
+// A scale whose largest value zero + scale * code would round past fp16's range
+// (past 65504 + 16, which would become inf) is lowered to what fits.
 template <int B, int F>
-__device__ inline __half2 fitting_scale(__half2 s, __half2 z) {
+__device__ __forceinline__ __half2 fitting(__half2 s, __half2 z) {
   const __half2 top = __hfma2(s, __float2half2_rn(largest_code<B, F>()), z);
-  if (__hisinf(__low2half(top)) || __hisinf(__high2half(top))) {
+  if (!__hble2(top, __float2half2_rn(65504.f))) {
     const float2 zf = __half22float2(z), sf = __half22float2(s);
     const float k = 1.f / largest_code<B, F>();
     s = __halves2half2(__float2half_rd(fminf(sf.x, (65504.f - zf.x) * k)),
@@ -226,69 +226,88 @@ __device__ inline __half2 fitting_scale(__half2 s, __half2 z) {
   return s;
 }
 
-// Pair k of word w as fp16 values.
+// Codes k of both half-words of w as fp16 numbers (float formats: their values).
+// A b-bit code at bit j of its half-word becomes 1024 + code * 2^j by setting the
+// exponent, j below a byte; one operation takes it back to the code, exactly.
 template <int B, int F>
-__device__ inline uint32_t value_pair(uint32_t w, int k, __half2 s, __half2 z) {
-  __half2 c;
+__device__ inline __half2 code_pair(uint32_t w, int k) {
   if constexpr (F == 1 && B != 2) {
-    const uint32_t x = unpack_float_pair<B>(w, k);
-    c = *reinterpret_cast<const __half2*>(&x);
+    return as_half2(unpack_float_pair<B>(w, k));
+  } else if constexpr (B == 8) {
+    return __hsub2(as_half2(unpack_pair<8>(w, k)), __float2half2_rn(1024.f));
   } else {
-    const uint32_t x = hsub2_bits(unpack_pair<B>(w, k), 0x64006400u);
-    c = *reinterpret_cast<const __half2*>(&x);
+    const int j = (B * k) % 8;
+    const uint32_t m = ((1u << B) - 1u) << j;
+    const __half2 x = as_half2(((w >> (B * k / 8 * 8)) & (m | (m << 16))) | 0x64006400u);
+    if (j == 0) return __hsub2(x, __float2half2_rn(1024.f));
+    const float f = 1.f / (float)(1 << j);
+    return __hfma2(x, __float2half2_rn(f), __float2half2_rn(-1024.f * f));
   }
-  const __half2 v = __hfma2(c, s, z);
-  return *reinterpret_cast<const uint32_t*>(&v);
 }
+
+// NW words of this lane's portion from byte o on.
+template <int LB, int NW>
+__device__ __forceinline__ void piece_words(const uint8_t* region, int o, uint32_t (&w)[NW]) {
+  const uint8_t* at = region + lane_off(threadIdx.x & 31, o, LB);
+  if constexpr (NW == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else if constexpr (NW == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(at);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
+  }
+}
+
+// The page writers below stay loops over eight-pair bodies.  Eight warps run
+// them for three classes next to the softmax and the products, and the
+// instruction cache is what limits them: with straight-line bodies (a quarter
+// fewer instructions) the kernel took 350 us instead of 280 on 512 rows x 65,536
+// keys x 8 heads.
 
 // Keys of one page-head: rows page * 16 + slot of the key tile.
 template <int D, int G, int B, int F>
-__device__ inline void write_keys(const uint8_t* blk, uint8_t* tile, int page) {
+__device__ __forceinline__ void write_keys(const uint8_t* blk, uint8_t* tile, int page) {
   constexpr int NG = D / G, LANE_BYTES = D * B / 16;
-  constexpr int PB = G * B / 32, NW = PB >= 4 ? PB / 4 : 1;
-  constexpr int U = LANE_BYTES < 16 ? LANE_BYTES : 16;
+  constexpr int PB = G * B / 32;                       // bytes of a piece (group, slot half)
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t* kpar = reinterpret_cast<const uint32_t*>(blk + 4 * D * B);
-  const uint8_t* kbase = blk + lane * U;
-  constexpr bool KALL = LANE_BYTES <= 32;
-  constexpr int KW = KALL ? LANE_BYTES / 4 : 2 * PB / 4;
-  uint32_t kw[KW];
-  if constexpr (KALL) lane_words<LANE_BYTES, KW>(kbase, 0, kw);
+  const uint32_t* kpar = reinterpret_cast<const uint32_t*>(blk + 4 * D * B) + g;
+  // a row's 16-byte chunks are exchanged with the row's number in its group of eight
+  uint8_t* dst = tile + page * (kPage * 128) + g * 128;
+  const int off = ((G == 64 ? 2 * t : t) ^ g) << 4;
+#pragma unroll 1
+  for (int y = 0; y < 2 * NG; ++y) {
+    const int gr = y >> 1, r = y & 1;
+    uint8_t* to = dst + (gr * G / 64) * (kTile * 128) + r * 1024;
+    const int first = G == 64 ? off : off ^ ((gr & 1) << 6);
+    if constexpr (B == 16) {
 #pragma unroll
-  for (int gr = 0; gr < NG; ++gr) {
-    if constexpr (!KALL) lane_words<LANE_BYTES, KW>(kbase, gr * 2 * PB / 4, kw);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      uint32_t w[NW];
-      if constexpr (PB == 2) {
-        const uint32_t h16 = (kw[gr] >> (16 * r)) & 0xFFFFu;
-        w[0] = (h16 & 0xFFu) | ((h16 & 0xFF00u) << 8);
+      for (int c = 0; c < G / 32; ++c) {
+        uint32_t w[4];
+        piece_words<LANE_BYTES, 4>(blk, y * PB + 16 * c, w);
+        *reinterpret_cast<uint4*>(to + (first ^ (c << 4))) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+      uint32_t w[PB >= 4 ? PB / 4 : 1];
+      if constexpr (PB == 2) {                         // 4 + 4 codes: bytes -> half-words
+        const uint32_t h16 = *reinterpret_cast<const uint16_t*>(blk + lane_off(lane, y * PB, LANE_BYTES));
+        w[0] = __byte_perm(h16, 0u, 0x4140);
       } else {
-#pragma unroll
-        for (int x = 0; x < NW; ++x) w[x] = kw[(KALL ? gr * 2 * NW : 0) + r * NW + x];
+        piece_words<LANE_BYTES, PB / 4>(blk, y * PB, w);
       }
-      __half2 s = __float2half2_rn(1.f), z = __float2half2_rn(0.f);
-      if constexpr (B < 16) {
-        const uint32_t par = kpar[gr * 16 + g + 8 * r];
-        const __half2 sz = *reinterpret_cast<const __half2*>(&par);
-        s = __low2half2(sz);
-        z = __high2half2(sz);
-        s = fitting_scale<B, F>(s, z);
-      }
-      constexpr int PAIRS = B == 16 ? 1 : (PB == 2 ? 4 : 16 / B);   // pairs of a word
-      const int row = page * kPage + g + 8 * r;
+      const __half2 sz = as_half2(kpar[gr * 16 + 8 * r]);
+      const __half2 z = __high2half2(sz), s = fitting<B, F>(__low2half2(sz), z);
+      constexpr int PAIRS = PB == 2 ? 4 : 16 / B;      // pairs of a word
 #pragma unroll
       for (int c = 0; c < G / 32; ++c) {               // 16-byte chunks of the piece
         uint32_t v[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int u = c * 4 + x;
-          if constexpr (B == 16) v[x] = w[u];
-          else v[x] = value_pair<B, F>(w[u / PAIRS], u % PAIRS, s, z);
+          v[x] = as_bits(__hfma2(code_pair<B, F>(w[u / PAIRS], u % PAIRS), s, z));
         }
-        const int ch = gr * G + t * (G / 4) + c * 8;   // first channel of the chunk
-        uint8_t* dst = tile + (ch / 64) * (kTile * 128) + row * 128 + ((((ch % 64) / 8) ^ (row & 7)) << 4);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4*>(to + (first ^ (c << 4))) = make_uint4(v[0], v[1], v[2], v[3]);
       }
     }
   }
@@ -296,55 +315,48 @@ __device__ inline void write_keys(const uint8_t* blk, uint8_t* tile, int page) {
 
 // Values of one page-head, transposed: row = channel, tokens along the row.
 template <int D, int G, int B, int F>
-__device__ inline void write_values(const uint8_t* blk, uint8_t* tile, int page, uint32_t mask) {
+__device__ __forceinline__ void write_values(const uint8_t* blk, uint8_t* tile, int page, uint32_t mask) {
   constexpr int NG = D / G, LANE_BYTES = D * B / 16;
   constexpr int Q = B == 16 ? D / 8 : D * B / 128;     // words per token pair
   constexpr int PER = B == 16 ? 1 : 16 / B;            // codes per half-word
-  constexpr int U = LANE_BYTES < 16 ? LANE_BYTES : 16;
+  constexpr int NW = B == 16 ? 4 : B / 2;              // words of a body: 64 channels (raw: 32)
+  constexpr int NB = Q / NW;                           // bodies per token pair
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t* vpar = reinterpret_cast<const uint32_t*>(blk + 4 * D * B + 64 * NG);
-  const uint8_t* vbase = blk + 2 * D * B + lane * U;
-  constexpr bool VALL = LANE_BYTES <= 32;
-  uint32_t vall[VALL ? LANE_BYTES / 4 : 1];
-  if constexpr (VALL) lane_words<LANE_BYTES, (VALL ? LANE_BYTES / 4 : 1)>(vbase, 0, vall);
-  // a dead slot's weight is 0, but what its bytes decode to may not be finite
-  const uint32_t tm = mask >> (2 * t);
-  const uint32_t dm[2] = {((tm & 1u) ? 0xFFFFu : 0u) | ((tm & 2u) ? 0xFFFF0000u : 0u),
-                          ((tm & 0x100u) ? 0xFFFFu : 0u) | ((tm & 0x200u) ? 0xFFFF0000u : 0u)};
-  uint8_t* base = tile + (page / 4) * (D * 128) + 4 * t;
+  const uint32_t* vpar = reinterpret_cast<const uint32_t*>(blk + 4 * D * B + 64 * NG) + 2 * t;
+  uint8_t* at = tile + (page / 4) * (D * 128) + g * 128 + 4 * t;
+  const int off = (((page % 4) * 2) ^ g) << 4;
+  // a dead slot's weight is 0, but what its bytes decode to may not be finite:
+  // its scale and zero become 0 (codes are finite), or the value (raw fp16, E4M3)
+  constexpr bool by_value = B == 16 || (B == 8 && F == 1);
+#pragma unroll 1
+  for (int y = 0; y < 2 * NB; ++y) {
+    const int P = y / NB, b = y % NB;
+    const uint32_t tm = mask >> (2 * t + 8 * P);
+    const uint32_t dm = ((tm & 1u) ? 0xFFFFu : 0u) | ((tm & 2u) ? 0xFFFF0000u : 0u);
+    uint8_t* to = at + (off ^ (P << 4)) + b * (NW * PER * 1024);
+    uint32_t w[NW];
+    piece_words<LANE_BYTES, NW>(blk + 2 * D * B, (P * Q + b * NW) * 4, w);
+    constexpr int GB = B == 16 ? 1 : 64 / G;           // groups of a body
+    __half2 s[GB], z[GB];
+    if constexpr (B < 16) {
 #pragma unroll
-  for (int P = 0; P < 2; ++P) {
-    const int chunk = (page % 4) * 2 + P;
-    uint8_t* at = base + g * 128 + ((chunk ^ g) << 4);
-    constexpr int HALF = Q >= 2 ? 2 : 1, QH = Q / HALF;
+      for (int gr = 0; gr < GB; ++gr) {
+        const uint32_t* pp = vpar + (b * GB + gr) * 16 + 8 * P;
+        const uint32_t p0 = pp[0], p1 = pp[1];
+        z[gr] = as_half2(__byte_perm(p0, p1, 0x7632) & dm);
+        s[gr] = fitting<B, F>(as_half2(__byte_perm(p0, p1, 0x5410) & dm), z[gr]);
+      }
+    }
 #pragma unroll
-    for (int hf = 0; hf < HALF; ++hf) {
-      uint32_t vr[QH];
-      if constexpr (VALL) {
-#pragma unroll
-        for (int x = 0; x < QH; ++x) vr[x] = vall[P * Q + hf * QH + x];
+    for (int x = 0; x < NW * PER; ++x) {               // channel 16 * (e / 2) + g + 8 * (e % 2), e from b on
+      uint32_t v;
+      if constexpr (B == 16) {
+        v = w[x];
       } else {
-        lane_words<LANE_BYTES, QH>(vbase, P * Q + hf * QH, vr);
+        const int gr = x * 8 / G;
+        v = as_bits(__hfma2(code_pair<B, F>(w[x / PER], x % PER), s[gr], z[gr]));
       }
-      __half2 s = __float2half2_rn(1.f), z = __float2half2_rn(0.f);
-#pragma unroll
-      for (int x = 0; x < QH * PER; ++x) {
-        const int e = hf * QH * PER + x;               // channel 16 * (e / 2) + g + 8 * (e % 2)
-        if constexpr (B < 16) {
-          if (x == 0 || (e * 8) % G == 0) {            // the next group's params
-            const int gr = e * 8 / G;
-            const uint32_t p0 = vpar[gr * 16 + 2 * t + 8 * P], p1 = vpar[gr * 16 + 2 * t + 8 * P + 1];
-            const uint32_t sb = __byte_perm(p0, p1, 0x5410), zb = __byte_perm(p0, p1, 0x7632);
-            s = *reinterpret_cast<const __half2*>(&sb);
-            z = *reinterpret_cast<const __half2*>(&zb);
-            s = fitting_scale<B, F>(s, z);
-          }
-        }
-        uint32_t v;
-        if constexpr (B == 16) v = vr[x];
-        else v = value_pair<B, F>(vr[x / PER], x % PER, s, z);
-        *reinterpret_cast<uint32_t*>(at + e * 1024) = v & dm[P];
-      }
+      *reinterpret_cast<uint32_t*>(to + x * 1024) = by_value ? v & dm : v;
     }
   }
 }
@@ -377,6 +389,80 @@ __device__ inline void write_page(const uint8_t* blk, uint32_t bits, uint8_t* ti
   }
 }
 
+// Scores of two pages: -inf for dead slots, whatever their keys decoded to.
+__device__ __forceinline__ void hide_dead(uint32_t (&s)[32], uint32_t live) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) s[e] = (live >> e) & 1u ? s[e] : 0xFF800000u;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction (each rounded as the single one).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)),
+        "l"(reinterpret_cast<const uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return d;
+}
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+  float a = __uint_as_float(s[0]), b = __uint_as_float(s[1]);
+#pragma unroll
+  for (int e = 2; e < 30; e += 4) {
+    a = max3(a, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+    b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+  }
+  return fmaxf(max3(a, __uint_as_float(s[30]), __uint_as_float(s[31])), b);
+}
+
+// P of 32 scores, 2^(s * scale - ref) in fp16, to 16 columns from `to` on; the
+// fp32 weights go into the running sums.
+__device__ __forceinline__ void weights32(const uint32_t (&s)[32], float scale, float ref, float2 (&add)[2],
+                                          uint32_t to) {
+  uint32_t pk[16];
+  const float2 k2 = make_float2(scale, scale), r2 = make_float2(-ref, -ref);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), k2, r2);
+    y.x = exp2_approx(y.x);
+    y.y = exp2_approx(y.y);
+    add[(e >> 1) & 1] = add2(add[(e >> 1) & 1], y);
+    pk[e / 2] = pack_half2_rn(y.x, y.y);
+  }
+  tmem_st16(to, pk);
+}
+
+// 1 in one lane of the (converged) warp, 0 in the others
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t lead;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(lead));
+  return lead;
+}
+
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
@@ -384,7 +470,9 @@ template <int D, int G>
 __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
   using S = Shape<D>;
   extern __shared__ uint8_t raw_smem[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+  // (an offset from the array, not a rounded address: a pointer made from an integer
+  // would be a generic one, and every access slower)
+  uint8_t* smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
   Misc* m = reinterpret_cast<Misc*>(smem + S::off_misc);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();                                   // the plan
@@ -403,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
   if (tid == 0) {
     for (int x = 0; x < kSlots; ++x) {
       mbar_init(&m->raw_full[x], 1);
-      mbar_init(&m->raw_empty[x], 1);
+      mbar_init(&m->raw_empty[x], kDequantWarps);
     }
     for (int x = 0; x < 6; ++x) {
       mbar_init(&m->kv_full[x], kDequantWarps);
@@ -424,72 +512,164 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
   tc_fence_after();
   const uint32_t tmem = m->tmem;
 
+  if (warp >= 16) {
+  fewer_regs<kRegsLast>();              // (one instruction for the whole warpgroup)
   if (warp == kWarpLoad) {
     // ---------------- loader ----------------
-    uint32_t seq = 0;                           // tiles so far
-    uint32_t head = 0, used = 0, oldest = 0;    // byte ring; oldest: first page whose bytes are held
-    uint32_t issued = 0;                        // pages handed to the ring
-    bool ok = true;
-    for (int64_t u = U0; ok && u < U1;) {
-      const Piece x = piece_at(p, nruns, u, U1, cta);
-      u += x.t1 - x.t0;
-      const int64_t row = (int64_t)x.run.prefix * p.max_blocks;
-      for (int64_t t = x.t0; ok && t < x.t1; t += 4) {
-        // 32 pages: descriptors and masks, a page per lane
-        const int64_t j = t * kTilePages + lane;
-        const int tiles = (int)min((int64_t)4, x.t1 - t);
-        uint64_t src = 0;
-        int cls = -1;
-        uint32_t mask = 0;
-        if (j < x.run.pages && lane < tiles * kTilePages) {
-          const uint64_t desc = p.live_list[row + j];
-          cls = entry_class(desc);
-          src = reinterpret_cast<uint64_t>(p.pool[cls]) +
-                ((uint64_t)entry_page(desc) * p.Hkv + x.h) * (uint64_t)p.phb[cls];
-          mask = entry_mask(p.table[row + live_desc_entry(desc)]);
-        }
-        for (int k = 0; ok && k < tiles * kTilePages; ++k) {
-          const uint64_t a = __shfl_sync(0xFFFFFFFFu, src, k);
-          const int c = __shfl_sync(0xFFFFFFFFu, cls, k);
-          const uint32_t mk = __shfl_sync(0xFFFFFFFFu, mask, k);
-          if (lane == 0) {
-            const uint32_t page = (seq + (k >> 3)) * kTilePages + (k & 7);
-            const uint32_t slot = page % kSlots;
-            const uint32_t bytes = c < 0 ? 0u : (uint32_t)p.phb[c];
-            const bool wrap = head + bytes > (uint32_t)S::ring;    // the rest of the ring is skipped
-            const uint32_t pad = wrap ? (uint32_t)S::ring - head : 0u;
-            // the slot's last page and enough bytes must have been given back
-            while (ok && (page - oldest >= (uint32_t)kSlots || used + pad + bytes > (uint32_t)S::ring)) {
-              ok = wait_role(m, &m->raw_empty[oldest % kSlots], (oldest / kSlots) & 1u);
-              used -= m->slot_size[oldest % kSlots];
-              ++oldest;
-            }
-            if (ok) {
-              if (wrap) head = 0;
-              m->slot_size[slot] = pad + bytes;
-              m->slot_off[slot] = head;
-              m->slot_bits[slot] = c < 0 ? 0u : ((uint32_t)p.bits[c] | (mk << 16));
-              if (bytes) {
-                mbar_arrive_expect_tx(&m->raw_full[slot], bytes);
-                bulk_g2s(smem + S::off_ring + head, reinterpret_cast<const void*>(a), bytes, &m->raw_full[slot]);
-              } else {
-                mbar_arrive(&m->raw_full[slot]);
-              }
-              head += bytes;
-              used += pad + bytes;
-              issued = page + 1;
-            }
-          }
-          ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
-        }
-        seq += tiles;
+    // Batches of up to four tiles, a page per lane; the descriptors of a batch are
+    // requested two batches ahead and the live masks one.
+    struct Batch {
+      int64_t row;                            // first entry of the prefix's lists
+      uint64_t desc;
+      uint32_t mask;
+      int h, tiles;
+    };
+    int64_t u = U0, t = 0;
+    Piece x;
+    x.t1 = 0;
+    auto fetch = [&]() {
+      Batch b;
+      b.tiles = 0;
+      b.mask = 0;
+      b.desc = ~0ull;
+      b.row = 0;
+      b.h = 0;
+      if (t >= x.t1) {
+        if (u >= U1) return b;
+        x = piece_at(p, nruns, u, U1, cta);
+        u += x.t1 - x.t0;
+        t = x.t0;
       }
+      b.row = (int64_t)x.run.prefix * p.max_blocks;
+      b.h = x.h;
+      b.tiles = (int)min((int64_t)4, x.t1 - t);
+      const int64_t j = t * kTilePages + lane;
+      if (lane < b.tiles * kTilePages && j < x.run.pages) b.desc = p.live_list[b.row + j];
+      t += b.tiles;
+      return b;
+    };
+    uint32_t seq = 0, head = 0, used = 0, oldest = 0;   // byte ring, in tiles: [oldest, seq) hold it
+    uint32_t held = 0;                        // lane l < kSlots: ring bytes of the tile in slot l
+    bool ok = true;
+    Batch cur, nxt;
+    cur.tiles = nxt.tiles = 0;
+    nxt.desc = ~0ull;
+    for (int ahead = 2; ok && (ahead > 0 || cur.tiles > 0); --ahead) {
+      if (nxt.desc != ~0ull) nxt.mask = entry_mask(p.table[nxt.row + live_desc_entry(nxt.desc)]);
+      const Batch after = fetch();
+      if (cur.tiles == 0) {                   // the first two rounds only fetch
+        cur = nxt;
+        nxt = after;
+        continue;
+      }
+      const bool page = cur.desc != ~0ull;
+      const int c = page ? entry_class(cur.desc) : 0;
+      const uint32_t bytes = page ? (uint32_t)p.phb[c] : 0u;
+      const uint64_t src = reinterpret_cast<uint64_t>(p.pool[c]) +
+                           ((uint64_t)entry_page(cur.desc) * p.Hkv + cur.h) * (uint64_t)p.phb[c];
+      uint32_t end = bytes;                   // prefix sums inside each tile's eight lanes
+#pragma unroll
+      for (int o = 1; o < kTilePages; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, end, o);
+        if ((lane & 7) >= o) end += y;
+      }
+      for (int k = 0; k < cur.tiles; ++k, ++seq) {
+        const uint32_t total = __shfl_sync(0xFFFFFFFFu, end, 8 * k + 7), slot = seq % kSlots;
+        uint32_t pad;
+        bool wrap;
+        while (true) {                        // until the slot and enough bytes have been given back
+          if (used == 0) head = 0;
+          wrap = head + total > (uint32_t)S::ring;
+          pad = wrap ? (uint32_t)S::ring - head : 0u;
+          if (seq - oldest < (uint32_t)kSlots && used + pad + total <= (uint32_t)S::ring) break;
+          if (!(ok = wait_warp(m, &m->raw_empty[oldest % kSlots], (oldest / kSlots) & 1u))) break;
+          used -= __shfl_sync(0xFFFFFFFFu, held, oldest % kSlots);
+          ++oldest;
+        }
+        if (!ok) break;
+        if (wrap) head = 0;
+        const uint32_t at = head + end - bytes;
+        if ((lane >> 3) == k) {
+          m->slot_off[slot][lane & 7] = at;
+          m->slot_bits[slot][lane & 7] = page ? ((uint32_t)p.bits[c] | (cur.mask << 16)) : 0u;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&m->raw_full[slot], total);
+        __syncwarp();
+        if ((lane >> 3) == k && page)
+          bulk_g2s(smem + S::off_ring + at, reinterpret_cast<const void*>(src), bytes, &m->raw_full[slot]);
+        if (lane == (int)slot) held = pad + total;
+        head += total;
+        used += pad + total;
+      }
+      cur = nxt;
+      nxt = after;
     }
     // every block in flight has landed before the CTA ends
     if (lane == 0)
-      for (uint32_t x = issued > kSlots ? issued - kSlots : 0; x < issued; ++x)
-        mbar_wait_bounded(&m->raw_full[x % kSlots], (x / kSlots) & 1u);
-  } else if (warp >= 8 && warp < 8 + kDequantWarps) {
+      for (uint32_t y = seq > kSlots ? seq - kSlots : 0; y < seq; ++y)
+        mbar_wait_bounded(&m->raw_full[y % kSlots], (y / kSlots) & 1u);
+  } else if (warp == kWarpMma) {
+    // ---------------- products ----------------
+    // The whole warp keeps the books, so that the operands are warp-uniform; one
+    // lane issues.
+    const uint32_t lead = elect_one();
+    uint32_t seq = 0, piece = 0, np[2] = {0, 0};
+    const uint64_t q_desc = operand_desc(smem_u32(smem + S::off_q)), kv_desc = operand_desc(smem_u32(smem + S::off_kv));
+    bool ok = true;
+    for (int64_t u = U0; ok && u < U1; ++piece) {
+      const Piece x = piece_at(p, nruns, u, U1, cta);
+      u += x.t1 - x.t0;
+      const uint32_t T = __shfl_sync(0xFFFFFFFFu, (uint32_t)(x.t1 - x.t0), 0);
+      const uint32_t pair = __shfl_sync(0xFFFFFFFFu, (uint32_t)x.pair, 0);
+      const uint32_t steps = T << pair;              // products of one group and one key tile
+      ok = wait_warp(m, &m->q_full, piece & 1u);
+      for (uint32_t s = 0; ok && s < steps + 2; ++s) {   // two scores ahead of the values
+        const uint32_t j = s & 1u;
+        if (s >= 2) {                                // O_j += P_j V
+          const uint32_t pos = 2 * (seq + ((s - 2) >> pair)) + 1, buf = pos % S::kv_bufs;
+          if (!pair || j == 0) ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
+          ok = ok && wait_warp(m, &m->p_full[j], np[j] & 1u);
+          if (!ok) break;
+          ++np[j];
+          tc_fence_after();
+          const uint64_t b = kv_desc + buf * (S::kv_bytes >> 4);
+          const uint32_t d = tmem + 256 + j * D, a = tmem + j * 128;
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts(d, a + k * 8, b + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), instr_desc(D), s >= 4 || k > 0);
+            if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
+            if (s >= steps) mma_commit(&m->o_full[j]);
+          }
+          __syncwarp();
+        }
+        if (s < steps) {                             // S_j = Q_j K^T
+          const uint32_t pos = 2 * (seq + (s >> pair)), buf = pos % S::kv_bufs;
+          if (!pair || j == 0) {
+            ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          const uint64_t a = q_desc + (pair ? j : 0u) * (S::q_bytes >> 4), b = kv_desc + buf * (S::kv_bytes >> 4);
+          const uint32_t d = tmem + j * 128;
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+              mma_ss(d, a + off, b + off, instr_desc(kTile), k > 0);
+            }
+            mma_commit(&m->s_full[j]);
+            if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
+          }
+          __syncwarp();
+        }
+      }
+      seq += T;
+    }
+  }
+  } else if (warp >= 8) {
+    fewer_regs<kRegsDequant>();
     // ---------------- codes -> fp16 operands ----------------
     const int page = warp - 8;
     uint32_t seq = 0;
@@ -498,10 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
       const Piece x = piece_at(p, nruns, u, U1, cta);
       u += x.t1 - x.t0;
       for (int64_t t = x.t0; t < x.t1; ++t, ++seq) {
-        const uint32_t n = seq * kTilePages + page, slot = n % kSlots;
-        if (!(ok = wait_warp(m, &m->raw_full[slot], (n / kSlots) & 1u))) break;
-        const uint32_t info = m->slot_bits[slot], bits = info & 0xFFFFu, mask = info >> 16;
-        const uint8_t* blk = smem + S::off_ring + m->slot_off[slot];
+        const uint32_t slot = seq % kSlots;
+        if (!(ok = wait_warp(m, &m->raw_full[slot], (seq / kSlots) & 1u))) break;
+        const uint32_t info = m->slot_bits[slot][page], bits = info & 0xFFFFu, mask = info >> 16;
+        const uint8_t* blk = smem + S::off_ring + m->slot_off[slot][page];
         uint32_t pos = 2 * seq, buf = pos % S::kv_bufs;
         if (!(ok = wait_warp(m, &m->kv_empty[buf], ((pos / S::kv_bufs) & 1u) ^ 1u))) break;
         if (lane == 0) m->mask[seq & 3][page] = (uint16_t)mask;
@@ -522,63 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
         }
       }
     }
-  } else if (warp == kWarpMma) {
-    // ---------------- products ----------------
-    if (lane == 0) {
-      uint32_t seq = 0, piece = 0, np[2] = {0, 0};
-      const uint32_t q_addr = smem_u32(smem + S::off_q), kv_addr = smem_u32(smem + S::off_kv);
-      bool ok = true;
-      for (int64_t u = U0; ok && u < U1; ++piece) {
-        const Piece x = piece_at(p, nruns, u, U1, cta);
-        const uint32_t T = (uint32_t)(x.t1 - x.t0);
-        u += T;
-        const uint32_t steps = x.pair ? 2 * T : T;   // products of one group and one key tile
-        ok = wait_role(m, &m->q_full, piece & 1u);
-        tc_fence_after();
-        auto qk = [&](uint32_t s) {
-          const uint32_t j = s & 1u, kt = x.pair ? s >> 1 : s, pos = 2 * (seq + kt), buf = pos % S::kv_bufs;
-          if (!x.pair || j == 0) {
-            ok = ok && wait_role(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
-            if (!ok) return;
-            tc_fence_after();
-          }
-          const uint32_t a = q_addr + (x.pair ? j : 0u) * S::q_bytes, b = kv_addr + buf * S::kv_bytes;
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * (128 * 128) + (k % 4) * 32;
-            mma_ss(tmem + j * 128, operand_desc(a + off), operand_desc(b + off), instr_desc(kTile), k > 0);
-          }
-          mma_commit(&m->s_full[j]);
-          if (!x.pair || j == 1) mma_commit(&m->kv_empty[buf]);
-        };
-        auto pv = [&](uint32_t s) {
-          const uint32_t j = s & 1u, kt = x.pair ? s >> 1 : s, pos = 2 * (seq + kt) + 1, buf = pos % S::kv_bufs;
-          if (!x.pair || j == 0) ok = ok && wait_role(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
-          ok = ok && wait_role(m, &m->p_full[j], np[j] & 1u);
-          if (!ok) return;
-          ++np[j];
-          tc_fence_after();
-          const uint32_t b = kv_addr + buf * S::kv_bytes;
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k) {
-            const uint32_t off = (k / 4) * (D * 128) + (k % 4) * 32;
-            mma_ts(tmem + 256 + j * D, tmem + j * 128 + k * 8, operand_desc(b + off), instr_desc(D),
-                   s >= 2 || k > 0);
-          }
-          if (!x.pair || j == 1) mma_commit(&m->kv_empty[buf]);
-          if (s + 2 >= steps) mma_commit(&m->o_full[j]);
-        };
-        if (ok) qk(0);
-        if (ok && steps > 1) qk(1);
-        for (uint32_t s = 0; ok && s < steps; ++s) {
-          pv(s);
-          if (ok && s + 2 < steps) qk(s + 2);
-        }
-        seq += T;
-      }
-    }
-    __syncwarp();
-  } else if (warp < 8) {
+  } else {
+    more_regs<kRegsSoftmax>();
     // ---------------- softmax ----------------
     const uint32_t j = warp >> 2;                    // group
     const int row = (warp & 3) * 32 + lane;          // row of the group's tile
@@ -614,28 +739,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
         if (!(ok = wait_warp(m, &m->s_full[j], ns & 1u))) break;
         ++ns;
         tc_fence_after();
-        uint32_t live[4];
-        {
-          const uint2* mp = reinterpret_cast<const uint2*>(m->mask[(seq + t) & 3]);
-          const uint2 m0 = mp[0], m1 = mp[1];
-          live[0] = m0.x; live[1] = m0.y; live[2] = m1.x; live[3] = m1.y;
-        }
-        const bool full = (live[0] & live[1] & live[2] & live[3]) == 0xFFFFFFFFu;
+        const uint4 live = *reinterpret_cast<const uint4*>(m->mask[(seq + t) & 3]);
+        const bool full = (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu;
         // ---- the row's maximum over the tile ----
         float mx = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tmem_ld32(t_s + c * 32, s);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t s0[32], s1[32];
+          tmem_ld32(t_s + c * 64, s0);
+          tmem_ld32(t_s + c * 64 + 32, s1);
           tc_wait_ld();
-          if (full) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(s[e]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              mx = fmaxf(mx, (live[c] >> e) & 1u ? __uint_as_float(s[e]) : -INFINITY);
+          if (!full) {
+            hide_dead(s0, c ? live.z : live.x);
+            hide_dead(s1, c ? live.w : live.y);
           }
+          mx = max3(mx, max32(s0), max32(s1));
         }
         mx *= p.scale_log2;
         // ---- move the reference where the maximum has outgrown it ----
@@ -658,27 +776,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
           ref = to;
         }
         // ---- P = 2^(s - ref), packed over the tile's own scores ----
-        float add[2] = {0.f, 0.f};
-#pragma unroll
+        float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {
-          uint32_t s[32], pk[16];
-          tmem_ld32(t_s + c * 32, s);
+          uint32_t s0[32];
+          tmem_ld32(t_s + c * 32, s0);
           tc_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float a = exp2_approx(fmaf(__uint_as_float(s[e]), p.scale_log2, -ref));
-            float b = exp2_approx(fmaf(__uint_as_float(s[e + 1]), p.scale_log2, -ref));
-            if (!full) {
-              a = (live[c] >> e) & 1u ? a : 0.f;
-              b = (live[c] >> (e + 1)) & 1u ? b : 0.f;
-            }
-            add[0] += a;
-            add[1] += b;
-            pk[e / 2] = pack_half2_rn(a, b);
-          }
-          tmem_st16(t_s + c * 16, pk);
+          if (!full) hide_dead(s0, c & 2 ? (c & 1 ? live.w : live.z) : (c & 1 ? live.y : live.x));
+          weights32(s0, p.scale_log2, ref, add, t_s + c * 16);
         }
-        sum += add[0] + add[1];
+        sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(&m->p_full[j]);
@@ -725,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
   if (warp == kWarpMma) {
     if (m->abort) {
       // products may still be in flight: a last commit covers them all
-      if (lane == 0) {
+      if (elect_one()) {
         set_status(p.status, THINKV_ERR_TIMEOUT);
         mma_commit(&m->drain);
         mbar_wait_bounded(&m->drain, 0);
