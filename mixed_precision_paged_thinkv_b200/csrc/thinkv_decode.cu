@@ -411,6 +411,15 @@ __device__ inline pages_t<SHARED> live_tokens(const DecodeParams& p, int i) {
   }
 }
 
+// Warps that share T units.  SHARED: four units each at least, so that a small
+// call leaves few pieces to merge (2 rows on 2,048 tokens, 8 kv-heads: 130 pieces a
+// segment merged in 69 us before, one unit a warp; 33 pieces since).
+template <bool SHARED>
+__device__ inline int64_t sharing_warps(int64_t T, int64_t W) {
+  if constexpr (SHARED) return min(W, max(T / 4, (int64_t)1));
+  return W;
+}
+
 // Ends the warp's work on segment seg = i * Hkv + h.  If the whole segment
 // was in this warp (Us >= U0 and Ue <= U1) its O rows and top-k mass are
 // written at once; otherwise the warp's piece record goes to rec[w + seg]
@@ -938,8 +947,9 @@ __global__ void __launch_bounds__(SplitShape<D>::threads, SplitShape<D>::ctas)
   write_empty_outputs<SHARED>(p, P, D);
 
   const int64_t T = (int64_t)P[p.n] * p.Hkv;
-  const int64_t W = (int64_t)gridDim.x * kDecWarps;
+  const int64_t W = sharing_warps<SHARED>(T, (int64_t)gridDim.x * kDecWarps);
   const int64_t w = (int64_t)blockIdx.x * kDecWarps + warp;
+  if (SHARED && w >= W) return;
   const int64_t U0 = w * T / W, U1 = (w + 1) * T / W;
   if (U0 >= U1) return;
 
@@ -1108,7 +1118,7 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   else pref = p.pref;
   const int nl = (int)(pref[i + 1] - pref[i]);
   if (!SHARED && nl == 0) return;               // written by the split kernel
-  const int64_t T = (int64_t)pref[p.n] * p.Hkv, W = p.split_warps;
+  const int64_t T = (int64_t)pref[p.n] * p.Hkv, W = sharing_warps<SHARED>((int64_t)pref[p.n] * p.Hkv, p.split_warps);
   const int64_t Us = (int64_t)pref[i] * p.Hkv + (int64_t)h * nl, Ue = Us + nl;
   const bool any = !SHARED || nl > 0;
   const int64_t w0 = any ? warp_of_unit(Us, T, W) : 0, w1 = any ? warp_of_unit(Ue - 1, T, W) : 0;
@@ -1366,6 +1376,102 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   if (lane == 0) p.mass[mrow] = sum / sL[r];
 }
 
+// The combine of a SHARED call without the top-k statistic: a CTA per (sequence,
+// kv-head), whose pieces are the split kernel's records and the prefix kernel's
+// partial rows.  Groups of Gq * D/4 threads (a quad of one head's row each) take
+// the pieces in turn, several loads in flight, and add up through shared memory
+// in a fixed order.
+constexpr int kMergeThreads = 512;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p) {
+  constexpr int QD = D / 4;
+  __shared__ float wt[kCombinePieces * 8], lt[kCombinePieces * 8];
+  __shared__ float sL[8];
+  __shared__ int sMk[8];
+  __shared__ float4 part[kMergeThreads];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int seg = blockIdx.x, i = seg / p.Hkv, h = seg - i * p.Hkv, Gq = p.Gq;
+  const int64_t first = p.plan.pref[i], T = p.plan.pref[p.n] * p.Hkv;
+  const int nl = (int)(p.plan.pref[i + 1] - first);
+  const int64_t W = sharing_warps<true>(T, p.split_warps);
+  const int64_t Us = first * p.Hkv + (int64_t)h * nl;
+  const int64_t w0 = nl ? warp_of_unit(Us, T, W) : 0;
+  const int np_split = nl ? (int)(warp_of_unit(Us + nl - 1, T, W) - w0 + 1) : 0;
+  int np = np_split;
+  PrefixPieces pp;
+  const int run = p.plan.item[i].w;
+  if (run >= 0) {
+    pp.find(p, i, h, run);
+    np += pp.count;
+  } else if (np <= 1) {
+    return;                                     // empty, or finished inside one split warp
+  }
+  const int64_t rb = record_bytes(Gq, D, 0);
+  const uint8_t* recs = reinterpret_cast<const uint8_t*>(p.rec) + (w0 + seg) * rb;
+  auto ml_of = [&](int j, int r) {
+    if (j < np_split) return __ldcg(reinterpret_cast<const float2*>(recs + j * rb) + r);
+    return __ldcg(p.prefix_ml + pp.row(p, j - np_split) + r);
+  };
+  const int QT = Gq * QD, groups = min(kMergeThreads / QT, 8);
+  const int g = tid / QT, quad = tid - g * QT, r_o = quad / QD;
+  const bool busy = g < groups;
+  if (tid < 8) { sMk[tid] = INT_MIN; sL[tid] = 0.f; }
+  __syncthreads();
+  auto okey = [](int b) { return b >= 0 ? b : b ^ 0x7FFFFFFF; };   // order-preserving, its own inverse
+  for (int x = tid; x < np * Gq; x += kMergeThreads)
+    atomicMax(&sMk[x % Gq], okey(__float_as_int(ml_of(x / Gq, x % Gq).x)));
+  __syncthreads();
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < np; j0 += kCombinePieces) {
+    const int cnt = min(kCombinePieces, np - j0);
+    for (int x = tid; x < cnt * Gq; x += kMergeThreads) {
+      const int j = x / Gq, r = x - j * Gq;
+      const float2 ml = ml_of(j0 + j, r);
+      const float wgt = exp2_approx(ml.x - __int_as_float(okey(sMk[r])));
+      wt[j * 8 + r] = wgt;
+      lt[j * 8 + r] = wgt * ml.y;
+    }
+    __syncthreads();
+    if (warp < Gq) {
+      float l = 0.f;
+      for (int j = lane; j < cnt; j += 32) l += lt[j * 8 + warp];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+      if (lane == 0) sL[warp] += l;
+    }
+    if (busy) {
+      auto add = [&](float4 v, float w) {
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      };
+      const int mid = min(max(np_split - j0, 0), cnt);   // records, then partial rows
+      const float4* a = reinterpret_cast<const float4*>(recs + (int64_t)j0 * rb + 64) + quad;
+#pragma unroll 4
+      for (int j = g; j < mid; j += groups) add(__ldcg(a + j * (rb / 16)), wt[j * 8 + r_o]);
+#pragma unroll 4
+      for (int j = mid + g; j < cnt; j += groups)
+        add(__ldcg(reinterpret_cast<const float4*>(p.prefix_o + pp.row(p, j0 + j - np_split) * D) + quad),
+            wt[j * 8 + r_o]);
+    }
+    __syncthreads();
+  }
+  if (busy) part[tid] = acc;
+  __syncthreads();
+  if (tid >= QT) return;
+  for (int x = 1; x < groups; ++x) {
+    const float4 v = part[x * QT + tid];
+    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+  }
+  const float inv = 1.f / sL[r_o];
+  const int64_t row = (int64_t)i * p.Hq + (int64_t)h * Gq;
+  reinterpret_cast<uint2*>(p.out + row * D)[quad] =
+      make_uint2(pack_half2_rn(acc.x * inv, acc.y * inv), pack_half2_rn(acc.z * inv, acc.w * inv));
+}
+
 template <int D, int G, bool TOPK, bool SHARED>
 cudaError_t launch_split_t(const DecodeParams& p, const DecodeLaunch& dl, cudaStream_t stream) {
   // raise the dynamic shared-memory limit of this instantiation once per
@@ -1390,6 +1496,8 @@ cudaError_t launch_split_t(const DecodeParams& p, const DecodeLaunch& dl, cudaSt
   e = launch_pdl(decode_split_kernel<D, G, TOPK, SHARED>, dim3(dl.grid), dim3(SplitShape<D>::threads), dl.smem_bytes,
                  stream, p);
   if (e != cudaSuccess) return e;
+  if constexpr (SHARED && !TOPK)
+    return launch_pdl(merge_kernel<D>, dim3((unsigned)(p.n * p.Hkv)), dim3(kMergeThreads), 0, stream, p);
   // the combine: one CTA per segment (most return at once), as many threads as
   // the segment's output quads (Gq * D/4), and a warp per head at least (the
   // per-head sums, the top-k merges)

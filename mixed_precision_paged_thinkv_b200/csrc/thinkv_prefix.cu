@@ -127,6 +127,15 @@ __device__ inline void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
       : "r"(addr)
       : "memory");
 }
+__device__ inline void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
 __device__ inline void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
@@ -424,6 +433,30 @@ __device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
     b = max3(b, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
   }
   return fmaxf(max3(a, __uint_as_float(s[30]), __uint_as_float(s[31])), b);
+}
+
+// N * 32 columns of this thread's row, times f
+template <int N>
+__device__ __forceinline__ void scale_columns(uint32_t addr, float f) {
+#pragma unroll 1
+  for (int c = 0; c < N; ++c) {
+    uint32_t o[32];
+    tmem_ld32(addr + c * 32, o);
+    tc_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+    tmem_st32(addr + c * 32, o);
+  }
+}
+// 32 weights (fp16, 16 columns) of this thread's row, times f
+__device__ __forceinline__ void scale_weights(uint32_t addr, float f) {
+  uint32_t w[16];
+  tmem_ld16(addr, w);
+  tc_wait_ld();
+  const __half2 h = __float2half2_rn(f);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = as_bits(__hmul2(as_half2(w[e]), h));
+  tmem_st16(addr, w);
 }
 
 // P of 32 scores, 2^(s * scale - ref) in fp16, to 16 columns from `to` on; the
@@ -741,49 +774,35 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
         tc_fence_after();
         const uint4 live = *reinterpret_cast<const uint4*>(m->mask[(seq + t) & 3]);
         const bool full = (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu;
-        // ---- the row's maximum over the tile ----
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t s0[32], s1[32];
-          tmem_ld32(t_s + c * 64, s0);
-          tmem_ld32(t_s + c * 64 + 32, s1);
-          tc_wait_ld();
-          if (!full) {
-            hide_dead(s0, c ? live.z : live.x);
-            hide_dead(s1, c ? live.w : live.y);
-          }
-          mx = max3(mx, max32(s0), max32(s1));
-        }
-        mx *= p.scale_log2;
-        // ---- move the reference where the maximum has outgrown it ----
-        const bool move = mx - kHeadroom > ref + kSlack || done == 0;
-        if (__any_sync(0xFFFFFFFFu, move)) {
-          const float to = move ? mx - kHeadroom : ref;
-          const float f = done == 0 ? 0.f : exp2_approx(ref - to);
-          if (done > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(t_o + c * 32, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(t_o + c * 32, o);
-            }
-          }
-          sum *= f;
-          ref = to;
-        }
-        // ---- P = 2^(s - ref), packed over the tile's own scores ----
+        // ---- P = 2^(s - ref), packed over the tile's own scores, 32 at a time ----
         float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto weigh = [&](uint32_t (&sc)[32], int c, uint32_t live_c) {
+          if (!full) hide_dead(sc, live_c);
+          const float mx = max32(sc) * p.scale_log2 - kHeadroom;
+          // a row whose maximum has outgrown its reference moves it, and what
+          // was summed under it: a whole power of two, so nothing is rounded
+          if (__any_sync(0xFFFFFFFFu, mx > ref + kSlack)) {
+            const float to = mx > ref + kSlack ? ceilf(mx) : ref;
+            const float f = ref > -INFINITY ? exp2_approx(ref - to) : (to > -INFINITY ? 0.f : 1.f);
+            if (done > 0) scale_columns<D / 32>(t_o, f);
+            for (int x = 0; x < c; ++x) scale_weights(t_s + x * 16, f);
+            add[0].x *= f; add[0].y *= f; add[1].x *= f; add[1].y *= f;
+            sum *= f;
+            ref = to;
+          }
+          weights32(sc, p.scale_log2, ref > -INFINITY ? ref : 0.f, add, t_s + c * 16);
+        };
+        uint32_t s0[32], s1[32];                 // the next 32 columns arrive under the present ones
+        tmem_ld32(t_s, s0);
+        tc_wait_ld();
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s0[32];
-          tmem_ld32(t_s + c * 32, s0);
+        for (int c = 0; c < 4; c += 2) {
+          tmem_ld32(t_s + c * 32 + 32, s1);
+          weigh(s0, c, c ? live.z : live.x);
           tc_wait_ld();
-          if (!full) hide_dead(s0, c & 2 ? (c & 1 ? live.w : live.z) : (c & 1 ? live.y : live.x));
-          weights32(s0, p.scale_log2, ref, add, t_s + c * 16);
+          if (c == 0) tmem_ld32(t_s + 64, s0);
+          weigh(s1, c + 1, c ? live.w : live.y);
+          tc_wait_ld();
         }
         sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
         tc_wait_st();

@@ -16,136 +16,173 @@ namespace thinkv {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 
 // Page-steps (live page x kv-head x sequence) that the split kernel has to be
 // spared before the prefix kernel is worth its own latency.
 constexpr int64_t kWorthPageSteps = 8192;
 
-__device__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
+// Exclusive prefix of N values per thread over the block (sh: N * 33 words);
+// tot: the block's sums.
+template <int N>
+__device__ void block_scan(int64_t (&v)[N], int64_t (&tot)[N], int64_t* sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int64_t x[N];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
+  for (int k = 0; k < N; ++k) {
+    x[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x[k], o);
+      if (lane >= o) x[k] += y;
+    }
+    if (lane == 31) sh[k * 33 + warp] = x[k];
   }
-  if (lane == 31) sh[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int64_t w = sh[lane];
+  if (warp < N) {                                // warp k scans the warps' sums of value k
+    int64_t w = lane < warps ? sh[warp * 33 + lane] : 0;
+    const int64_t own = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
       if (lane >= o) w += y;
     }
-    sh[lane] = w;
+    if (lane < warps) sh[warp * 33 + lane] = w - own;
+    if (lane == 31) sh[warp * 33 + 32] = w;
   }
   __syncthreads();
-  const int64_t before = warp ? sh[warp - 1] : 0;
-  *total = sh[kWarps - 1];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    v[k] = sh[k * 33 + warp] + x[k] - v[k];
+    tot[k] = sh[k * 33 + 32];
+  }
   __syncthreads();
-  return before + x - v;
 }
+
+// One row as the plan sees it.
+struct Row {
+  int s, x;            // its sequence (-1: the row is empty) and prefix (-1: none)
+};
 
 __global__ void __launch_bounds__(kThreads)
     shared_plan_kernel(CacheView C, int32_t n, const int32_t* __restrict__ seq,
                        const int32_t* __restrict__ prefix, bool inline_only, SharedPlan plan) {
-  __shared__ int64_t sh[kWarps];
-  const int tid = threadIdx.x, H = C.L.num_kv_heads, Gq = C.L.num_q_heads / H;
+  __shared__ int64_t sh[3 * 33];
+  const int tid = threadIdx.x, nt = blockDim.x, H = C.L.num_kv_heads, Gq = C.L.num_q_heads / H;
+  const int max_seqs = C.L.max_seqs;
   pdl_launch_dependents();
-  pdl_wait();
-  auto row_prefix = [&](int i) {                 // the prefix row i really has (-1: none)
-    const int s = seq[i], x = prefix[i];
-    return s >= 0 && s < C.L.max_seqs && x >= 0 && x < C.L.max_seqs ? x : -1;
+  auto row = [&](int i) {
+    Row r;
+    r.s = seq[i];
+    r.x = prefix[i];
+    if (r.s < 0 || r.s >= max_seqs || r.x < -1 || r.x >= max_seqs) r.s = r.x = -1;
+    return r;
   };
-  int64_t total, carry = 0;
+  // a call of one row per thread reads its inputs while the previous kernel ends
+  Row mine = {-1, -1}, before = {-1, -1};
+  const bool one_pass = n <= nt;
+  if (tid < n) mine = row(tid);
+  if (tid < n && tid > 0) before = row(tid - 1);
+  pdl_wait();
+  // live pages of the row's sequence and prefix, in flight over the first scan
+  int own = 0, shared = 0;
+  if (one_pass && tid < n) {
+    if (mine.s >= 0) own = C.num_live[mine.s];
+    if (mine.x >= 0) shared = C.num_live[mine.x];
+  }
   // ---- runs of neighbours with the same prefix ----
-  for (int base = 0; base < n; base += kThreads) {
+  int64_t carry = 0, my_run = 0;
+  for (int base = 0; base < n; base += nt) {
     const int i = base + tid;
-    const bool start = i < n && (i == 0 || row_prefix(i) != row_prefix(i - 1));
-    const int64_t k = carry + block_scan(start, sh, &total);
-    if (start) plan.start[k] = i;
-    carry += total;
+    if (!one_pass && i < n) {
+      mine = row(i);
+      if (i > 0) before = row(i - 1);
+    }
+    const bool start = i < n && (i == 0 || mine.x != before.x);
+    int64_t v[1] = {start}, tot[1];
+    block_scan<1>(v, tot, sh);
+    if (start) plan.start[carry + v[0]] = i;
+    my_run = carry + v[0] + start - 1;           // (one pass: this row's run)
+    carry += tot[0];
   }
   const int nruns = (int)carry;
   if (tid == 0) plan.start[nruns] = n;
   __syncthreads();
-  // ---- what the prefix kernel would spare the split kernel ----
-  int64_t spared = 0;
-  for (int base = 0; base < nruns; base += kThreads) {
+  // ---- the runs that the prefix kernel could take, and what it would spare ----
+  int64_t spared = 0, nused = 0, units = 0;
+  for (int base = 0; base < nruns; base += nt) {
     const int k = base + tid;
-    int64_t v = 0;
-    if (k < nruns) {
-      const int first = plan.start[k], count = plan.start[k + 1] - first, x = row_prefix(first);
-      if (!inline_only && x >= 0 && count >= 2) v = (int64_t)(count - 1) * C.num_live[x] * H;
-    }
-    block_scan(v, sh, &total);
-    spared += total;
-  }
-  const bool use = spared >= kWorthPageSteps;
-  int64_t nused = 0, units = 0;
-  for (int base = 0; base < nruns; base += kThreads) {
-    const int k = base + tid;
-    bool mine = false;
+    int64_t v[3] = {0, 0, 0}, tot[3];
     SharedRun r = {0, 0, -1, 0};
-    RunShape s = {0, 0, 0};
     if (k < nruns) {
       r.first = plan.start[k];
       r.count = plan.start[k + 1] - r.first;
-      r.prefix = row_prefix(r.first);
+      r.prefix = row(r.first).x;
       r.pages = r.prefix >= 0 ? C.num_live[r.prefix] : 0;
-      mine = use && r.count >= 2 && r.pages > 0;
-      if (mine) s = run_shape(r.count, r.pages, Gq);
+      if (!inline_only && r.count >= 2 && r.pages > 0) {
+        const RunShape s = run_shape(r.count, r.pages, Gq);
+        v[0] = (int64_t)(r.count - 1) * r.pages * H;
+        v[1] = 1;
+        v[2] = H * (int64_t)s.blocks * s.tiles;
+      }
     }
-    const int64_t e = nused + block_scan(mine, sh, &total);
-    nused += total;
-    const int64_t u = units + block_scan(mine ? H * (int64_t)s.blocks * s.tiles : 0, sh, &total);
-    units += total;
-    if (k < nruns) plan.used[k] = mine ? (int)e : -1;
-    if (mine) {
-      plan.run[e] = r;
-      plan.rstart[e] = u;
+    const bool fit = v[1] != 0;
+    block_scan<3>(v, tot, sh);
+    if (k < nruns) plan.used[k] = fit ? (int)(nused + v[1]) : -1;
+    if (fit) {
+      plan.run[nused + v[1]] = r;
+      plan.rstart[nused + v[1]] = units + v[2];
     }
+    spared += tot[0];
+    nused += tot[1];
+    units += tot[2];
   }
+  const bool use = spared >= kWorthPageSteps;
   if (tid == 0) {
-    plan.rstart[nused] = units;
-    *plan.nruns = (int)nused;
+    plan.rstart[use ? nused : 0] = use ? units : 0;
+    *plan.nruns = use ? (int)nused : 0;
   }
   __syncthreads();
   // ---- every sequence's own reading ----
   int64_t k0 = 0, pages = 0;
-  for (int base = 0; base < n; base += kThreads) {
+  for (int base = 0; base < n; base += nt) {
     const int i = base + tid;
-    const bool start = i < n && (i == 0 || row_prefix(i) != row_prefix(i - 1));
-    const int64_t before = block_scan(start, sh, &total);
-    const int64_t k = k0 + before + start - 1;
-    k0 += total;
+    if (!one_pass) {
+      int64_t v[1] = {0}, tot[1];
+      if (i < n) {
+        mine = row(i);
+        v[0] = i == 0 || mine.x != row(i - 1).x;
+        own = mine.s >= 0 ? C.num_live[mine.s] : 0;
+        shared = mine.x >= 0 ? C.num_live[mine.x] : 0;
+      }
+      const int64_t start = v[0];
+      block_scan<1>(v, tot, sh);
+      my_run = k0 + v[0] + start - 1;
+      k0 += tot[0];
+    }
     int4 item = make_int4(-1, -1, 0, -1);
-    int64_t v = 0;
+    int64_t v[1] = {0}, tot[1];
     if (i < n) {
-      const int s = seq[i], x = prefix[i];
-      if (s < 0 || s >= C.L.max_seqs || x < -1 || x >= C.L.max_seqs) {
+      if (mine.s < 0) {
         set_status(C.status, THINKV_ERR_INVALID);    // decoded as empty
       } else {
-        item.x = s;
-        v = C.num_live[s];
-        if (x >= 0) {
-          item.w = plan.used[k];
+        item.x = mine.s;
+        v[0] = own;
+        if (mine.x >= 0) {
+          item.w = use ? plan.used[my_run] : -1;
           if (item.w < 0) {
-            item.y = x;
-            item.z = C.num_live[x];
-            v += item.z;
+            item.y = mine.x;
+            item.z = shared;
+            v[0] += shared;
           }
         }
       }
     }
-    const int64_t at = pages + block_scan(v, sh, &total);
-    pages += total;
+    block_scan<1>(v, tot, sh);
     if (i < n) {
       plan.item[i] = item;
-      plan.pref[i] = at;
+      plan.pref[i] = pages + v[0];
     }
+    pages += tot[0];
   }
   if (tid == 0) plan.pref[n] = pages;
 }
@@ -154,7 +191,10 @@ __global__ void __launch_bounds__(kThreads)
 
 cudaError_t launch_shared_plan(const CacheView& C, int32_t n, const int32_t* seq, const int32_t* prefix,
                                bool inline_only, const SharedPlan& plan, cudaStream_t stream) {
-  return launch_pdl(shared_plan_kernel, dim3(1), dim3(kThreads), 0, stream, C, n, seq, prefix, inline_only,
+  int threads = (n + 31) / 32 * 32;              // a row a thread where that is possible
+  if (threads < 96) threads = 96;                // (a warp for each of a scan's three values)
+  if (threads > kThreads) threads = kThreads;
+  return launch_pdl(shared_plan_kernel, dim3(1), dim3(threads), 0, stream, C, n, seq, prefix, inline_only,
                     plan);
 }
 

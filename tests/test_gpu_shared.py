@@ -288,9 +288,11 @@ def test_same_as_one_sequence():
     q = torch.randn(2, c.Hq, c.d, device="cuda").half()
     a = c.decode(_ids([0, 2]), q)[0]
     b = c.decode_shared(_ids([0, 2]), _ids([-1, -1]), q)[0]
-    assert torch.equal(a, b)
     e = c.decode_shared(_ids([1, 1]), _ids([0, 2]), q)[0]
-    assert torch.equal(a, e)
+    ref, _, bound = Exact(c).rows([0, 2], [-1, -1], q.cpu().numpy())
+    for out in (a, b, e):                              # the calls split the work differently
+        _within(out, ref, bound)
+    assert torch.equal(b, e)
 
 
 def test_bad_ids_decode_as_empty():
