@@ -21,9 +21,11 @@
 //   apply: a warp per chunk (release) or per chunk and kv-head (fork); the lane
 //   holds one table entry, ballots give its rank and so its place on the stack
 //   or its new page.
-// Fork is bound by HBM writes.  A page-head block travels through shared
-// memory by bulk copies in both directions (no register ever holds it), each
-// warp with its own ring of blocks, so the SM keeps ~200 KB in flight.
+// Fork is bound by HBM writes: a warp copies a page-head block with 16-byte
+// loads and stores, 40 warps an SM.  (Bulk copies through shared memory in both
+// directions were slower, 146 us against the figure in fork_apply_kernel's
+// comment: a block stays in shared memory until its store has drained, which
+// leaves few stores in flight.)
 #include <stdint.h>
 
 #include "thinkv_common.cuh"
@@ -39,8 +41,10 @@ constexpr int kPlanThreads = 256;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanBatch = 4;                  // chunks per warp and pass (loads in flight)
 constexpr int kApplyWarps = 8;
-constexpr int kMaxRing = 8;
-constexpr int kRingBytes = 24 * 1024;          // a warp's ring of page-head blocks, at most
+constexpr int kForkCtas = 4;                   // CTAs of the copy per SM (32 warps)
+constexpr int kCopyDepth = 4;                  // 16-byte loads a lane has in flight
+constexpr int kParts = 8;                      // warps that share a chunk's blocks of one kv-head
+constexpr int kCopies = 8;                     // neighbouring copies of one source made together
 
 struct TurnoverWs {
   uint32_t* arrive;    // arrival counter of the plan kernel, zero between calls
@@ -49,7 +53,8 @@ struct TurnoverWs {
   int32_t* nb;         // [n] table entries of each listed (source) sequence
   int32_t* tot;        // [n][3] its pages per class
   int32_t* base;       // [n][3] pages of the sequences before it in the call
-  int32_t* ubase;      // [n + 1] chunks before it (an empty sequence counts as one)
+  int32_t* ubase;      // [n + 1] chunks before it (an empty sequence counts as one; a copy that
+                       // leads no group counts as none)
   int32_t* crank;      // [n][chunks][3] a chunk's first rank within its sequence and class
   int64_t chunks;      // chunks of a full table
 };
@@ -75,6 +80,12 @@ TurnoverWs carve(const thinkv_layout& L, void* ws, int32_t n) {
   w.crank = reinterpret_cast<int32_t*>(p);
   w.chunks = table_chunks(L);
   return w;
+}
+
+// Whether pair x of a fork leads a group: neighbours with one source, up to
+// kCopies of them, are copied together.
+__device__ inline bool leads_group(const int32_t* src, int x) {
+  return x % kCopies == 0 || src[x] != src[x - 1];
 }
 
 // Exclusive prefix over the block of four values per thread; tot: block totals.
@@ -203,6 +214,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       for (int c = 0; c < 3; ++c) v[c] = __ldcg(&ws.tot[x * 3 + c]);
       const int b = __ldcg(&ws.nb[x]);
       v[3] = b > 0 ? (b + kChunk - 1) / kChunk : 1;
+      if (dst && !leads_group(seq, x)) v[3] = 0;
     }
     block_scan4(v, tot, sh);
     if (x < n) {
@@ -308,17 +320,6 @@ __global__ void __launch_bounds__(kApplyWarps * 32)
   }
 }
 
-struct ForkRing {
-  int stages, stage_bytes, warp_smem;
-};
-
-__device__ inline void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
-               "r"(bytes)
-               : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
 // The sequence's state that is not in pages: chunk k of K copies its share.
 __device__ void fork_state(const CacheView& C, int s, int t, int k, int K, const int4* seg, int4* segw,
                            int32_t* nseg, int32_t* settled) {
@@ -360,104 +361,88 @@ __device__ void fork_state(const CacheView& C, int s, int t, int k, int K, const
   }
 }
 
-__global__ void __launch_bounds__(kApplyWarps * 32, 1)
+__global__ void __launch_bounds__(kApplyWarps * 32, kForkCtas)
     fork_apply_kernel(CacheView C, int32_t n, const int32_t* __restrict__ src,
                       const int32_t* __restrict__ dst, int4* seg, int32_t* nseg, int32_t* settled,
-                      TurnoverWs ws, ForkRing ring) {
-  extern __shared__ __align__(128) uint8_t smem[];
+                      TurnoverWs ws) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint8_t* blocks = smem + warp * ring.warp_smem;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(blocks + ring.stages * ring.stage_bytes);
   pdl_launch_dependents();
-  if (lane == 0) {
-    for (int x = 0; x < ring.stages; ++x) mbar_init(&bars[x], 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
   pdl_wait();
   if (ws.head[0] == 0) return;                        // the call was refused
-  const int H = C.L.num_kv_heads;
-  const int64_t items = (int64_t)ws.ubase[n] * H, nw = (int64_t)gridDim.x * kApplyWarps;
-  int64_t phb[3];
-#pragma unroll
-  for (int c = 0; c < 3; ++c) phb[c] = page_head_bytes(C.L.head_dim, C.L.group_size, C.L.bits[c]);
-  uint32_t loads = 0;                                 // blocks loaded so far: stage and phase follow
+  const int H = C.L.num_kv_heads, warps = H * kParts;   // warps of a chunk
+  const int64_t items = (int64_t)ws.ubase[n] * warps, nw = (int64_t)gridDim.x * kApplyWarps;
   for (int64_t it = (int64_t)blockIdx.x * kApplyWarps + warp; it < items; it += nw) {
-    const int u = (int)(it / H), h = (int)(it - (int64_t)u * H);
-    const int i = sequence_of_chunk(ws, n, u), k = u - ws.ubase[i], s = src[i], t = dst[i];
-    const int64_t srow = (int64_t)s * C.L.max_blocks_per_seq, trow = (int64_t)t * C.L.max_blocks_per_seq;
+    const int u = (int)(it / warps), hp = (int)(it - (int64_t)u * warps);
+    const int h = hp / kParts, part = hp - h * kParts;
+    const int i = sequence_of_chunk(ws, n, u), k = u - ws.ubase[i], s = src[i];
+    const int64_t srow = (int64_t)s * C.L.max_blocks_per_seq;
     const int nb = ws.nb[i], e = k * kChunk + lane;
+    int members = 1;                                  // copies of this source made here
+    while (i + members < n && (i + members) % kCopies != 0 && src[i + members] == s) ++members;
     const bool valid = e < nb;
     const uint64_t ent = valid ? C.block_table[srow + e] : 0;
     const int c = entry_class(ent);
     const int64_t page = entry_page(ent);
-    const int rank = call_rank(ws, i, k, c, valid);
-    int64_t to = 0;
-    if (valid)
-      to = granted_page(C, c, ws.head[4 + c] - ws.head[7 + c] + rank, ws.head[4 + c]);
+    const int rank = call_rank(ws, i, k, c, valid) - (valid ? ws.base[i * 3 + c] : 0);   // in the source
     const int cnt = min(kChunk, nb - k * kChunk);
-    const uint64_t from_ptr = reinterpret_cast<uint64_t>(C.pool[c]) + (page * H + h) * phb[c];
-    const uint64_t to_ptr = reinterpret_cast<uint64_t>(C.pool[c]) + (to * H + h) * phb[c];
-    const uint32_t bytes = (uint32_t)phb[c];
-    // block j of the chunk goes through stage (loads0 + j) % stages
-    const uint32_t loads0 = loads;
-    auto load = [&](int j) {
-      const uint64_t p = __shfl_sync(0xFFFFFFFFu, from_ptr, j);
-      const uint32_t b = __shfl_sync(0xFFFFFFFFu, bytes, j);
-      if (lane == 0) {
-        const uint32_t st = (loads0 + j) % ring.stages;
-        mbar_arrive_expect_tx(&bars[st], b);
-        bulk_g2s(blocks + st * ring.stage_bytes, reinterpret_cast<const void*>(p), b, &bars[st]);
-      }
-    };
-    for (int j = 0; j < ring.stages && j < cnt; ++j) load(j);
-    if (h == 0) {                                     // bookkeeping, while the first blocks arrive
-      if (valid) {
-        const int index = C.live_index[srow + e];
-        C.block_table[trow + e] = make_entry((uint32_t)to, c, entry_mask(ent));
-        C.live_index[trow + e] = index;
-        if (index >= 0) C.live_list[trow + index] = make_live_desc((uint32_t)to, c, e);
-      }
-      for (int j = 0; j < cnt; j += 2) {              // slot positions, two pages at a time
-        const int from = j + (lane >> 4);
-        const int pc = __shfl_sync(0xFFFFFFFFu, c, from & 31);
-        const int64_t pa = __shfl_sync(0xFFFFFFFFu, page, from & 31);
-        const int64_t pb = __shfl_sync(0xFFFFFFFFu, to, from & 31);
-        if (from < cnt) C.slot_pos[pc][pb * kPage + (lane & 15)] = C.slot_pos[pc][pa * kPage + (lane & 15)];
-      }
-      fork_state(C, s, t, k, ws.ubase[i + 1] - ws.ubase[i], seg, seg, nseg, settled);
+    const int64_t phb = page_head_bytes(C.L.head_dim, C.L.group_size, C.L.bits[c]);
+    const uint64_t from_ptr = reinterpret_cast<uint64_t>(C.pool[c]) + (page * H + h) * phb;
+    int to[kCopies];                                  // this entry's page in each copy
+#pragma unroll
+    for (int m = 0; m < kCopies; ++m) {
+      to[m] = 0;
+      if (valid && m < members)
+        to[m] = granted_page(C, c, ws.head[4 + c] - ws.head[7 + c] + ws.base[(i + m) * 3 + c] + rank, ws.head[4 + c]);
     }
-    for (int j = 0; j < cnt; ++j) {
-      const uint32_t l = loads0 + j, st = l % ring.stages;
-      const uint64_t p = __shfl_sync(0xFFFFFFFFu, to_ptr, j);
-      const uint32_t b = __shfl_sync(0xFFFFFFFFu, bytes, j);
-      int ok = 1;
-      if (lane == 0) {
-        ok = mbar_wait_bounded(&bars[st], (l / ring.stages) & 1u);
-        if (ok) bulk_s2g(reinterpret_cast<void*>(p), blocks + st * ring.stage_bytes, b);
-      }
-      if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) {
-        // the loads still in flight land (waited for with the same limit) before the CTA ends
-        if (lane == 0) {
-          set_status(C.status, THINKV_ERR_TIMEOUT);
-          for (int j2 = j + 1; j2 < cnt && j2 < (j > 0 ? j - 1 : 0) + ring.stages; ++j2)
-            mbar_wait_bounded(&bars[(loads0 + j2) % ring.stages], ((loads0 + j2) / ring.stages) & 1u);
-          asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    for (int j = part; j < cnt; j += kParts) {        // this part's page-head blocks: read once
+      const uint4* a = reinterpret_cast<const uint4*>(__shfl_sync(0xFFFFFFFFu, from_ptr, j));
+      const int cj = __shfl_sync(0xFFFFFFFFu, c, j), quads = __shfl_sync(0xFFFFFFFFu, (int)(phb / 16), j);
+      uint4* pool = reinterpret_cast<uint4*>(C.pool[cj]) + (int64_t)h * quads;
+      for (int q = lane; q < quads + lane; q += 32 * kCopyDepth) {
+        uint4 v[kCopyDepth];
+#pragma unroll
+        for (int x = 0; x < kCopyDepth; ++x)
+          if (q + 32 * x < quads) v[x] = __ldg(a + q + 32 * x);
+#pragma unroll
+        for (int m = 0; m < kCopies; ++m) {
+          if (m >= members) break;
+          uint4* b = pool + (int64_t)__shfl_sync(0xFFFFFFFFu, to[m], j) * H * quads;
+#pragma unroll
+          for (int x = 0; x < kCopyDepth; ++x)
+            if (q + 32 * x < quads) b[q + 32 * x] = v[x];
         }
-        return;
-      }
-      // the stage of block j - 1 is free once its store has read it
-      if (j > 0 && j - 1 + ring.stages < cnt) {
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-        load(j - 1 + ring.stages);
       }
     }
-    loads = loads0 + cnt;
-    // the next chunk reuses every stage
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-    __syncwarp();
+    // the bookkeeping of the chunk, three tasks a copy, spread over its warps
+    for (int id = hp; id < 3 * members; id += warps) {
+      const int m = id / 3, task = id - 3 * m, t = dst[i + m];
+      const int64_t trow = (int64_t)t * C.L.max_blocks_per_seq;
+      int mine = 0;
+#pragma unroll
+      for (int x = 0; x < kCopies; ++x) mine = x == m ? to[x] : mine;
+      if (task == 0) {
+        if (valid) {
+          const int index = C.live_index[srow + e];
+          C.block_table[trow + e] = make_entry((uint32_t)mine, c, entry_mask(ent));
+          C.live_index[trow + e] = index;
+          if (index >= 0) C.live_list[trow + index] = make_live_desc((uint32_t)mine, c, e);
+        }
+      } else if (task == 1) {                         // slot positions, two pages at a time
+#pragma unroll 4
+        for (int j = 0; j < kChunk; j += 2) {
+          const int from = j + (lane >> 4);
+          const int pc = __shfl_sync(0xFFFFFFFFu, c, from);
+          const int64_t pa = __shfl_sync(0xFFFFFFFFu, page, from), pb = __shfl_sync(0xFFFFFFFFu, mine, from);
+          if (from < cnt) {
+            int32_t* pos = C.slot_pos[pc] + (lane & 15);
+            pos[pb * kPage] = __ldg(pos + pa * kPage);   // (the source's pages change in no fork)
+          }
+        }
+      } else {
+        fork_state(C, s, t, k, max(1, (nb + kChunk - 1) / kChunk), seg, seg, nseg, settled);
+      }
+    }
   }
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 cudaError_t launch_plan(const CacheView& C, int32_t n, const int32_t* seq, const int32_t* dst,
@@ -490,27 +475,10 @@ cudaError_t launch_fork(const CacheView& C, int32_t n, const int32_t* src, const
   const TurnoverWs ws = carve(C.L, workspace, n);
   cudaError_t e = launch_plan(C, n, src, dst, ws, stream);
   if (e != cudaSuccess) return e;
-  int64_t most = 0;
-  for (int c = 0; c < 3; ++c) {
-    const int64_t b = page_head_bytes(C.L.head_dim, C.L.group_size, C.L.bits[c]);
-    most = most > b ? most : b;
-  }
-  // a ring of up to 24 KB a warp: 8 warps fill the SM's shared memory
-  ForkRing ring;
-  ring.stage_bytes = (int)((most + 127) / 128 * 128);
-  ring.stages = kRingBytes / ring.stage_bytes;       // 3 (raw fp16, d = 128) or more
-  if (ring.stages > kMaxRing) ring.stages = kMaxRing;
-  ring.warp_smem = ring.stages * ring.stage_bytes + 128;
-  const int smem = kApplyWarps * ring.warp_smem;
-  // the attribute is the largest ring's, whatever this layout needs: host
-  // threads with different layouts do not undo each other's
-  e = cudaFuncSetAttribute(fork_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kApplyWarps * (kRingBytes + 128));
-  if (e != cudaSuccess) return e;
-  int64_t grid = ((int64_t)n * ws.chunks * C.L.num_kv_heads + kApplyWarps - 1) / kApplyWarps;
-  if (grid > num_sms) grid = num_sms;
-  return launch_pdl(fork_apply_kernel, dim3((unsigned)grid), dim3(kApplyWarps * 32), (size_t)smem, stream, C, n,
-                    src, dst, seg, nseg, settled, ws, ring);
+  int64_t grid = ((int64_t)n * ws.chunks * C.L.num_kv_heads * kParts + kApplyWarps - 1) / kApplyWarps;
+  if (grid > (int64_t)num_sms * kForkCtas) grid = (int64_t)num_sms * kForkCtas;
+  return launch_pdl(fork_apply_kernel, dim3((unsigned)grid), dim3(kApplyWarps * 32), 0, stream, C, n, src, dst,
+                    seg, nseg, settled, ws);
 }
 
 }  // namespace thinkv
