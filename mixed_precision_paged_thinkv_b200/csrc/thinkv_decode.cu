@@ -1384,6 +1384,7 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
 constexpr int kMergeThreads = 512;
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p) {
+  const int nt = blockDim.x;
   constexpr int QD = D / 4;
   __shared__ float wt[kCombinePieces * 8], lt[kCombinePieces * 8];
   __shared__ float sL[8];
@@ -1414,19 +1415,19 @@ __global__ void __launch_bounds__(kMergeThreads, 2) merge_kernel(DecodeParams p)
     if (j < np_split) return __ldcg(reinterpret_cast<const float2*>(recs + j * rb) + r);
     return __ldcg(p.prefix_ml + pp.row(p, j - np_split) + r);
   };
-  const int QT = Gq * QD, groups = min(kMergeThreads / QT, 8);
+  const int QT = Gq * QD, groups = nt / QT;
   const int g = tid / QT, quad = tid - g * QT, r_o = quad / QD;
   const bool busy = g < groups;
   if (tid < 8) { sMk[tid] = INT_MIN; sL[tid] = 0.f; }
   __syncthreads();
   auto okey = [](int b) { return b >= 0 ? b : b ^ 0x7FFFFFFF; };   // order-preserving, its own inverse
-  for (int x = tid; x < np * Gq; x += kMergeThreads)
+  for (int x = tid; x < np * Gq; x += nt)
     atomicMax(&sMk[x % Gq], okey(__float_as_int(ml_of(x / Gq, x % Gq).x)));
   __syncthreads();
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j0 = 0; j0 < np; j0 += kCombinePieces) {
     const int cnt = min(kCombinePieces, np - j0);
-    for (int x = tid; x < cnt * Gq; x += kMergeThreads) {
+    for (int x = tid; x < cnt * Gq; x += nt) {
       const int j = x / Gq, r = x - j * Gq;
       const float2 ml = ml_of(j0 + j, r);
       const float wgt = exp2_approx(ml.x - __int_as_float(okey(sMk[r])));
@@ -1497,7 +1498,14 @@ cudaError_t launch_split_t(const DecodeParams& p, const DecodeLaunch& dl, cudaSt
                  stream, p);
   if (e != cudaSuccess) return e;
   if constexpr (SHARED && !TOPK)
-    return launch_pdl(merge_kernel<D>, dim3((unsigned)(p.n * p.Hkv)), dim3(kMergeThreads), 0, stream, p);
+  {
+    // four groups of Gq * D/4 threads, at least a warp a head
+    int mt = (4 * p.Gq * (D / 4) + 31) / 32 * 32;
+    if (mt < 32 * p.Gq) mt = 32 * p.Gq;
+    if (mt < 128) mt = 128;
+    if (mt > kMergeThreads) mt = kMergeThreads;
+    return launch_pdl(merge_kernel<D>, dim3((unsigned)(p.n * p.Hkv)), dim3(mt), 0, stream, p);
+  }
   // the combine: one CTA per segment (most return at once), as many threads as
   // the segment's output quads (Gq * D/4), and a warp per head at least (the
   // per-head sums, the top-k merges)
