@@ -7,6 +7,7 @@ shared library is missing or cannot be loaded, importing ``lib()`` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 import threading
@@ -75,6 +76,7 @@ class TbeStruct(C.Structure):
 
 _lock = threading.Lock()
 _lib = None
+_NO_GUARD = contextlib.nullcontext()
 
 
 def lib():
@@ -231,6 +233,9 @@ class ThinKVCache:
                 nbytes = int(L.thinkv_tbe_buffer_bytes(C.byref(self.layout), i))
                 self.tbe_buf[name] = self._buffer(name, nbytes, buffers)
             self.tbe = TbeStruct(*[_ptr(self.tbe_buf[n]) for n in TBE_BUFFERS])
+        self._lib, self._cs_ref = L, C.byref(self.cs)
+        self._tbe_ref = None if self.tbe is None else C.byref(self.tbe)
+        self._where, self._sizes = self.buf["status"].device, {}
         if buffers is None:
             self.reset()
 
@@ -350,59 +355,61 @@ class ThinKVCache:
 
     def release(self, seq: torch.Tensor, stream=None):
         """The sequences `seq` (distinct) end: their pages go back to the pools."""
-        n = int(seq.numel())
+        n = seq.numel()
         self._expect(seq, torch.int32, n)
         if n == 0:
             return
         with self._guard():
-            st = self._stream_here(stream)
-            ws = self._counter_workspace("turnover", self._turnover_bytes(n), st)
-            _check(lib().thinkv_release(C.byref(self.cs), self._tbe_ref(), n, _ptr(seq), _ptr(ws), ws.numel(),
-                                        st.cuda_stream), "release")
+            ws = self._turnover_workspace(n, stream)
+            _check(self._lib.thinkv_release(self._cs_ref, self._tbe_ref, n, seq.data_ptr(), ws.data_ptr(),
+                                            ws.numel(), self._raw_stream(stream)), "release")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Sequence dst[i] (empty; distinct) becomes a copy of src[i]."""
-        n = int(src.numel())
+        n = src.numel()
         self._expect(src, torch.int32, n)
         self._expect(dst, torch.int32, n)
         if n == 0:
             return
         with self._guard():
-            st = self._stream_here(stream)
-            ws = self._counter_workspace("turnover", self._turnover_bytes(n), st)
-            _check(lib().thinkv_fork(C.byref(self.cs), self._tbe_ref(), n, _ptr(src), _ptr(dst), _ptr(ws),
-                                     ws.numel(), st.cuda_stream), "fork")
-
-    def _turnover_bytes(self, n: int) -> int:
-        nbytes = int(lib().thinkv_turnover_workspace_bytes(C.byref(self.layout), n))
-        if nbytes == 0:
-            raise ThinkvError(ERR_INVALID, f"{n} sequences in one call of a cache of {self.max_seqs}")
-        return nbytes
-
-    def _tbe_ref(self):
-        return None if self.tbe is None else C.byref(self.tbe)
+            ws = self._turnover_workspace(n, stream)
+            _check(self._lib.thinkv_fork(self._cs_ref, self._tbe_ref, n, src.data_ptr(), dst.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), self._raw_stream(stream)), "fork")
 
     def _expect(self, t: torch.Tensor, dtype, numel: int):
-        assert t.dtype == dtype and t.is_contiguous() and t.numel() == numel
-        assert t.device == self.buf["status"].device, f"tensor on {t.device}, cache on {self.device}"
+        assert t.dtype == dtype and t.numel() == numel and t.is_contiguous()
+        assert t.device == self._where, f"tensor on {t.device}, cache on {self._where}"
 
     def _guard(self):
         # kernels are launched on the cache's device, whichever is current
-        return torch.cuda.device(self.buf["status"].device)
+        if torch.cuda.current_device() == self._where.index:
+            return _NO_GUARD
+        return torch.cuda.device(self._where)
 
-    def _stream_here(self, stream):
-        return stream if stream is not None else torch.cuda.current_stream()
+    def _raw_stream(self, stream) -> int:
+        return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
-    def _counter_workspace(self, key: str, nbytes: int, stream) -> torch.Tensor:
-        """A workspace whose arrival counter is zeroed once, in the order of `stream`.  Its first
-        use cannot be inside a graph capture: the zero fill would only run when the graph does."""
-        t = self._ws.get(key)
+    def _sized(self, name: str, *args) -> int:
+        """A workspace size, asked for once per set of arguments."""
+        n = self._sizes.get((name, args))
+        if n is None:
+            n = int(getattr(self._lib, name)(C.byref(self.layout), *args))
+            if n == 0:
+                raise ThinkvError(ERR_INVALID, f"{name}{args}")
+            self._sizes[(name, args)] = n
+        return n
+
+    def _turnover_workspace(self, n: int, stream) -> torch.Tensor:
+        """Its arrival counter is zeroed once, in the order of the call's stream.  The first use
+        cannot be inside a graph capture: the zero fill would only run when the graph does."""
+        nbytes = self._sized("thinkv_turnover_workspace_bytes", n)
+        t = self._ws.get("turnover")
         if t is None or t.numel() < nbytes:
             if torch.cuda.is_current_stream_capturing():
-                raise ThinkvError(ERR_WORKSPACE, f"{key}: run the call once before capturing it")
+                raise ThinkvError(ERR_WORKSPACE, "turnover: run the call once before capturing it")
             with torch.cuda.stream(stream):
-                t = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.buf["status"].device)
-            self._ws[key] = t
+                t = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self._where)
+            self._ws["turnover"] = t
         return t
 
     def decode_workspace_bytes(self, n: int, topk: int = 0) -> int:
@@ -429,14 +436,14 @@ class ThinKVCache:
 
     def decode_shared_workspace_bytes(self, n: int, topk: int = 0) -> int:
         with self._guard():
-            return int(lib().thinkv_decode_shared_workspace_bytes(C.byref(self.layout), n, topk))
+            return int(self._lib.thinkv_decode_shared_workspace_bytes(C.byref(self.layout), n, topk))
 
     def decode_shared(self, seq: torch.Tensor, prefix: torch.Tensor, q: torch.Tensor,
                       topk: Optional[int] = None, softmax_scale: float = 0.0,
                       out: Optional[torch.Tensor] = None, mass: Optional[torch.Tensor] = None, stream=None):
         """Decode attention over the tokens of prefix[i] (-1: none) and of seq[i]
         together; neighbouring rows with the same prefix read it once."""
-        n, topk = int(seq.numel()), int(topk or 0)
+        n, topk = seq.numel(), int(topk or 0)
         self._expect(seq, torch.int32, n)
         self._expect(prefix, torch.int32, n)
         self._expect(q, torch.float16, n * self.Hq * self.d)
@@ -445,19 +452,17 @@ class ThinKVCache:
         if topk and mass is not None:
             self._expect(mass, torch.float32, n * self.Hq)
         with self._guard():
-            st = self._stream_here(stream)
-            nbytes = self.decode_shared_workspace_bytes(n, topk)
-            if nbytes == 0:
-                raise ThinkvError(ERR_INVALID, "decode_shared workspace size")
-            with torch.cuda.stream(st):
+            nbytes = self._sized("thinkv_decode_shared_workspace_bytes", n, topk)
+            with (_NO_GUARD if stream is None else torch.cuda.stream(stream)):
                 if out is None:
-                    out = torch.empty(n, self.Hq, self.d, dtype=torch.float16, device=q.device)
+                    out = torch.empty((n, self.Hq, self.d), dtype=torch.float16, device=self._where)
                 if topk and mass is None:
-                    mass = torch.empty(n, self.Hq, dtype=torch.float32, device=q.device)
+                    mass = torch.empty((n, self.Hq), dtype=torch.float32, device=self._where)
                 ws = self._workspace("decode_shared", nbytes)
-            _check(lib().thinkv_decode_shared(C.byref(self.cs), n, _ptr(seq), _ptr(prefix), _ptr(q), _ptr(out),
-                                              _ptr(mass) if topk else None, topk, float(softmax_scale),
-                                              _ptr(ws), ws.numel(), st.cuda_stream), "decode_shared")
+            _check(self._lib.thinkv_decode_shared(
+                self._cs_ref, n, seq.data_ptr(), prefix.data_ptr(), q.data_ptr(), out.data_ptr(),
+                mass.data_ptr() if topk else None, topk, float(softmax_scale), ws.data_ptr(), ws.numel(),
+                self._raw_stream(stream)), "decode_shared")
         return out, (mass if topk else None)
 
     def status(self, stream=None) -> int:

@@ -1670,9 +1670,11 @@ cudaError_t launch_decode(const CacheView& C, int32_t n, const int32_t* seq, con
   return launch_kernels(p, L.head_dim, L.group_size, false, dl, stream);
 }
 
-// The prefix kernel takes one CTA per SM; a call with the top-k statistic or of
-// one sequence has no use for it.
-static bool with_prefix_kernel(int32_t n, int32_t topk) { return n > 1 && topk == 0; }
+// Whether the prefix kernel could be worth its launch: not with the top-k
+// statistic, nor where even a full table shared by the whole call spares too little.
+static bool with_prefix_kernel(const thinkv_layout& L, int32_t n, int32_t topk) {
+  return topk == 0 && (int64_t)(n - 1) * L.max_blocks_per_seq * L.num_kv_heads >= kWorthPageSteps;
+}
 
 size_t decode_shared_workspace_bytes(const thinkv_layout& L, int32_t n, int32_t topk, int num_sms,
                                      const DecodeLaunch& dl) {
@@ -1681,7 +1683,7 @@ size_t decode_shared_workspace_bytes(const thinkv_layout& L, int32_t n, int32_t 
              round256((size_t)(n / 2 + 1) * sizeof(SharedRun)) + round256((size_t)(n / 2 + 2) * 8) +
              2 * round256(((size_t)n + 1) * 4);
   b += round256((size_t)dl.pieces * (size_t)record_bytes(Gq, L.head_dim, topk));
-  if (with_prefix_kernel(n, topk)) {
+  if (with_prefix_kernel(L, n, topk)) {
     const size_t rows = (size_t)partial_rows(L, n, num_sms);
     b += round256(rows * sizeof(float2)) + rows * L.head_dim * 4;
   }
@@ -1709,7 +1711,7 @@ cudaError_t launch_decode_shared(const CacheView& C, int32_t n, const int32_t* s
   p.plan.start = reinterpret_cast<int32_t*>(take(((size_t)n + 1) * 4));
   p.plan.used = reinterpret_cast<int32_t*>(take(((size_t)n + 1) * 4));
   p.rec = take((size_t)dl.pieces * (size_t)record_bytes(p.Gq, D, p.topk));
-  const bool with_prefix = with_prefix_kernel(n, p.topk);
+  const bool with_prefix = with_prefix_kernel(L, n, p.topk);
   cudaError_t e = launch_shared_plan(C, n, seq, prefix, !with_prefix, p.plan, stream);
   if (e != cudaSuccess) return e;
   if (with_prefix) {

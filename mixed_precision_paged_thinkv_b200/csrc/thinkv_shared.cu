@@ -17,10 +17,6 @@ namespace {
 
 constexpr int kThreads = 1024;
 
-// Page-steps (live page x kv-head x sequence) that the split kernel has to be
-// spared before the prefix kernel is worth its own latency.
-constexpr int64_t kWorthPageSteps = 8192;
-
 // Exclusive prefix of N values per thread over the block (sh: N * 33 words);
 // tot: the block's sums.
 template <int N>

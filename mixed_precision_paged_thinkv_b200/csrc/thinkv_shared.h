@@ -12,6 +12,10 @@ namespace thinkv {
 constexpr int kTilePages = 8;                 // pages of a key tile (128 tokens)
 constexpr int kBlockRows = 256;               // query rows of a prefix block, at most
 
+// Page-steps (live page x kv-head x sequence) that the split kernel has to be
+// spared before the prefix kernel is worth its own latency.
+constexpr int64_t kWorthPageSteps = 8192;
+
 // One run of neighbours with the same prefix whose prefix goes through the
 // prefix kernel.
 struct SharedRun {
