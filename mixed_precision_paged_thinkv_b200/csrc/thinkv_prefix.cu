@@ -750,16 +750,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
       u += T;
       // ---- queries: this group's 128 rows (a small block's rows by group 0) ----
       if (x.pair || j == 0) {
-        const int lo = j * 128;
-        for (int i = tid & 127; i < 128 * (D / 8); i += 128) {
-          const int r = i / (D / 8), c = i % (D / 8), lr = lo + r;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (lr < x.rows) {
-            const int mem = x.first_member + lr / p.Gq, hd = x.h * p.Gq + lr % p.Gq;
-            v = *reinterpret_cast<const uint4*>(p.q + ((int64_t)mem * p.Hq + hd) * D + c * 8);
+        // Rows of consecutive sequences: D/8 lanes a row, eight loads in flight each
+        constexpr int RL = D / 8, RS = 128 / RL;        // lanes of a row, rows of a step
+        const int c = tid % RL, r0 = (tid & 127) / RL;
+        const uint32_t inv = 65536u / (uint32_t)p.Gq + 1;   // lr / Gq for lr < 256, Gq <= 8
+        uint8_t* dst = smem + S::off_q + j * S::q_bytes + (c / 8) * (128 * 128);
+#pragma unroll 1
+        for (int y = 0; y < 128 / RS; y += 8) {
+          uint4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int lr = j * 128 + r0 + (y + k) * RS;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (lr < x.rows) {
+              const int in = (int)(((uint32_t)lr * inv) >> 16), hd = x.h * p.Gq + lr - in * p.Gq;
+              v[k] = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)(x.first_member + in) * p.Hq + hd) * D) + c);
+            }
           }
-          *reinterpret_cast<uint4*>(smem + S::off_q + j * S::q_bytes + (c / 8) * (128 * 128) + r * 128 +
-                                    (((c % 8) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int r = r0 + (y + k) * RS;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((c % 8) ^ (r & 7)) << 4)) = v[k];
+          }
         }
         fence_proxy_async_smem();
       }
