@@ -402,3 +402,35 @@ def test_back_to_back_calls():
     for (s, p), q, out in zip(calls, qs, outs):
         ref, _, bound = exact.rows(s, p, q.cpu().numpy())
         _within(out, ref, bound)
+
+
+@pytest.mark.parametrize("n,heads", [(1500, "tiny"), (3000, "gqa8"), (16384, "tiny")])
+def test_large_calls(n, heads):
+    """More rows than the plan has threads, up to the largest call: runs of every length,
+    rows that share a sequence, rows without a prefix; a sample of the rows is compared."""
+    rng = np.random.default_rng(n)
+    lens = [700, 260, 90, 1] + [int(x) for x in rng.integers(0, 50, 60)]
+    c = _fill(heads, "842", lens, seed=16, holes=0.1)
+    prefix = np.repeat(rng.integers(-1, 4, n), rng.integers(1, 300, n))[:n]
+    seq = rng.integers(4, 64, n)
+    q = rng.standard_normal((n, c.Hq, c.d)).astype(np.float16)
+    out, _ = c.decode_shared(_ids(seq.tolist()), _ids(prefix.tolist()), torch.from_numpy(q).cuda())
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    pick = np.unique(np.concatenate([rng.integers(0, n, 400), [0, 1023, 1024, n - 1]]))
+    ref, _, bound = Exact(c).rows(seq[pick].tolist(), prefix[pick].tolist(), q[pick])
+    _within(out[torch.from_numpy(pick).cuda()], ref, bound)
+
+
+def test_many_rows_with_topk():
+    c = _fill("tiny", "float", [300, 40] + [20] * 10, seed=17)
+    rng = np.random.default_rng(3)
+    n = 1300
+    prefix, seq = np.repeat(rng.integers(-1, 2, 13), 100), rng.integers(2, 12, n)
+    q = rng.standard_normal((n, c.Hq, c.d)).astype(np.float16)
+    out, mass = c.decode_shared(_ids(seq.tolist()), _ids(prefix.tolist()), torch.from_numpy(q).cuda(), topk=8)
+    torch.cuda.synchronize()
+    pick = rng.integers(0, n, 200)
+    ref, rmass, bound = Exact(c).rows(seq[pick].tolist(), prefix[pick].tolist(), q[pick], topk=8)
+    _within(out[torch.from_numpy(pick).cuda()], ref, bound)
+    assert np.abs(mass.cpu().numpy()[pick] - rmass).max() <= Hn.MASS_TOL
