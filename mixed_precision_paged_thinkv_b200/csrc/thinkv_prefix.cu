@@ -60,6 +60,12 @@ struct Shape {
   static constexpr int q_bytes = 128 * D * 2;               // one query tile
   static constexpr int kv_bufs = D == 128 ? 3 : 6;
   static constexpr int ring = 65536;                        // raw bytes in flight
+  // tensor memory: score tiles (two, or three where the accumulators leave room:
+  // a group's next scores are then made while it still weighs the present ones),
+  // then the groups' accumulators
+  static constexpr int s_bufs = D == 128 ? 2 : 3;
+  static constexpr int col_o = s_bufs * kTile;
+  static_assert(col_o + 2 * D <= 512, "tensor memory columns");
   static constexpr int off_q = 0;
   static constexpr int off_kv = 2 * q_bytes;
   static constexpr int off_ring = off_kv + kv_bufs * kv_bytes;
@@ -70,7 +76,9 @@ struct Shape {
 struct Misc {
   uint64_t raw_full[kSlots], raw_empty[kSlots];
   uint64_t kv_full[6], kv_empty[6];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full, drain;
+  uint64_t s_full[3], p_full[3];              // of the score tiles
+  uint64_t o_done[2][2];                      // [group][odd]: products, counted per group
+  uint64_t q_full, drain;
   uint32_t slot_off[kSlots][kTilePages];      // where each page's block lies in the ring
   uint32_t slot_bits[kSlots][kTilePages];     // its class's bits | live mask << 16 (0: no page)
   alignas(16) uint16_t mask[4][kTilePages];   // live masks of the last four tiles
@@ -126,6 +134,16 @@ __device__ inline void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr)
       : "memory");
+}
+// Waits for this thread's loads; r, the registers of one of them, are used after it.
+__device__ inline void tc_wait_ld_of(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), 
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), 
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), 
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 __device__ inline void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
@@ -442,7 +460,7 @@ __device__ __forceinline__ void scale_columns(uint32_t addr, float f) {
   for (int c = 0; c < N; ++c) {
     uint32_t o[32];
     tmem_ld32(addr + c * 32, o);
-    tc_wait_ld();
+    tc_wait_ld_of(o);
 #pragma unroll
     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
     tmem_st32(addr + c * 32, o);
@@ -530,11 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
       mbar_init(&m->kv_full[x], kDequantWarps);
       mbar_init(&m->kv_empty[x], 1);
     }
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < 3; ++x) {
       mbar_init(&m->s_full[x], 1);
       mbar_init(&m->p_full[x], 128);
-      mbar_init(&m->o_full[x], 1);
     }
+    for (int x = 0; x < 4; ++x) mbar_init(&m->o_done[x >> 1][x & 1], 1);
     mbar_init(&m->q_full, 256);
     mbar_init(&m->drain, 1);
     m->abort = 0;
@@ -647,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
     // The whole warp keeps the books, so that the operands are warp-uniform; one
     // lane issues.
     const uint32_t lead = elect_one();
-    uint32_t seq = 0, piece = 0, np[2] = {0, 0};
+    uint32_t seq = 0, piece = 0, base = 0;           // tiles, pieces, steps before this piece
+    uint32_t odd = 0;                                // bit j: group j's next product has an odd number
     const uint64_t q_desc = operand_desc(smem_u32(smem + S::off_q)), kv_desc = operand_desc(smem_u32(smem + S::off_kv));
     bool ok = true;
     for (int64_t u = U0; ok && u < U1; ++piece) {
@@ -657,47 +676,50 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
       const uint32_t pair = __shfl_sync(0xFFFFFFFFu, (uint32_t)x.pair, 0);
       const uint32_t steps = T << pair;              // products of one group and one key tile
       ok = wait_warp(m, &m->q_full, piece & 1u);
-      for (uint32_t s = 0; ok && s < steps + 2; ++s) {   // two scores ahead of the values
-        const uint32_t j = s & 1u;
-        if (s >= 2) {                                // O_j += P_j V
-          const uint32_t pos = 2 * (seq + ((s - 2) >> pair)) + 1, buf = pos % S::kv_bufs;
+      constexpr uint32_t NS = S::s_bufs;             // scores are made NS steps ahead of the values
+      for (uint32_t s = 0; ok && s < steps + NS; ++s) {
+        if (s >= NS) {                               // O_j += P_j V
+          const uint32_t r = s - NS, j = r & 1u, pos = 2 * (seq + (r >> pair)) + 1, buf = pos % S::kv_bufs;
+          const uint32_t g = base + r, sb = g % NS;
           if (!pair || j == 0) ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
-          ok = ok && wait_warp(m, &m->p_full[j], np[j] & 1u);
+          ok = ok && wait_warp(m, &m->p_full[sb], (g / NS) & 1u);
           if (!ok) break;
-          ++np[j];
           tc_fence_after();
           const uint64_t b = kv_desc + buf * (S::kv_bytes >> 4);
-          const uint32_t d = tmem + 256 + j * D, a = tmem + j * 128;
+          const uint32_t d = tmem + S::col_o + j * D, a = tmem + sb * kTile;
           if (lead) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(d, a + k * 8, b + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), instr_desc(D), s >= 4 || k > 0);
+              mma_ts(d, a + k * 8, b + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), instr_desc(D), r >= 2 || k > 0);
             if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
-            if (s >= steps) mma_commit(&m->o_full[j]);
+            mma_commit(&m->o_done[j][(odd >> j) & 1u]);
           }
+          odd ^= 1u << j;
           __syncwarp();
         }
         if (s < steps) {                             // S_j = Q_j K^T
-          const uint32_t pos = 2 * (seq + (s >> pair)), buf = pos % S::kv_bufs;
+          const uint32_t j = s & 1u, pos = 2 * (seq + (s >> pair)), buf = pos % S::kv_bufs;
+          const uint32_t sb = (base + s) % NS;
           if (!pair || j == 0) {
             ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
             if (!ok) break;
           }
           tc_fence_after();
           const uint64_t a = q_desc + (pair ? j : 0u) * (S::q_bytes >> 4), b = kv_desc + buf * (S::kv_bytes >> 4);
-          const uint32_t d = tmem + j * 128;
+          const uint32_t d = tmem + sb * kTile;
           if (lead) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
               mma_ss(d, a + off, b + off, instr_desc(kTile), k > 0);
             }
-            mma_commit(&m->s_full[j]);
+            mma_commit(&m->s_full[sb]);
             if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
           }
           __syncwarp();
         }
       }
+      base += steps;
       seq += T;
     }
   }
@@ -740,9 +762,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
     // ---------------- softmax ----------------
     const uint32_t j = warp >> 2;                    // group
     const int row = (warp & 3) * 32 + lane;          // row of the group's tile
-    const uint32_t t_s = tmem + j * 128 + ((uint32_t)(warp & 3) << 21);
-    const uint32_t t_o = tmem + 256 + j * D + ((uint32_t)(warp & 3) << 21);
-    uint32_t seq = 0, ns = 0, no = 0, piece = 0;
+    const uint32_t t_row = tmem + ((uint32_t)(warp & 3) << 21), t_o = t_row + S::col_o + j * D;
+    uint32_t seq = 0, piece = 0, base = 0, no = 0;   // tiles, pieces, steps, products of the group so far
+    // Product i of the group is done.  Two barriers take turns: a wait sees only
+    // the parity of the phase, and the product before the awaited one may or may not be done.
+    auto wait_product = [&](uint32_t i) { return wait_warp(m, &m->o_done[j][i & 1u], (i >> 1) & 1u); };
     bool ok = true;
     for (int64_t u = U0; ok && u < U1; ++piece) {
       const Piece x = piece_at(p, nruns, u, U1, cta);
@@ -776,14 +800,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
         fence_proxy_async_smem();
       }
       mbar_arrive(&m->q_full);
+      // Both groups are past the piece before: every earlier phase of the score
+      // tiles is over, so that the parities below mean this piece's (and a group
+      // without a step arrives in the right phase the next time).
+      if (!(ok = wait_warp(m, &m->q_full, piece & 1u))) break;
 
       float ref = -INFINITY, sum = 0.f;
-      const uint32_t first = x.pair ? 0 : j, step = x.pair ? 1 : 2;
+      const uint32_t steps = x.pair ? 2 * T : T;
       uint32_t done = 0;
-      for (uint32_t t = first; t < T; t += step, ++done) {
-        if (!(ok = wait_warp(m, &m->s_full[j], ns & 1u))) break;
-        ++ns;
+      for (uint32_t r = j; r < steps; r += 2, ++done) {
+        constexpr uint32_t NS = S::s_bufs;
+        const uint32_t t = x.pair ? r >> 1 : r, sb = (base + r) % NS;
+        if (!(ok = ok && wait_warp(m, &m->s_full[sb], ((base + r) / NS) & 1u))) break;
         tc_fence_after();
+        const uint32_t t_s = t_row + sb * kTile;
         const uint4 live = *reinterpret_cast<const uint4*>(m->mask[(seq + t) & 3]);
         const bool full = (live.x & live.y & live.z & live.w) == 0xFFFFFFFFu;
         // ---- P = 2^(s - ref), packed over the tile's own scores, 32 at a time ----
@@ -796,7 +826,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
           if (__any_sync(0xFFFFFFFFu, mx > ref + kSlack)) {
             const float to = mx > ref + kSlack ? ceilf(mx) : ref;
             const float f = ref > -INFINITY ? exp2_approx(ref - to) : (to > -INFINITY ? 0.f : 1.f);
-            if (done > 0) scale_columns<D / 32>(t_o, f);
+            if (done > 0) {                      // the group's last product may still be running
+              ok = ok && wait_product(no + done - 1);
+              tc_fence_after();
+              scale_columns<D / 32>(t_o, f);
+            }
             for (int x = 0; x < c; ++x) scale_weights(t_s + x * 16, f);
             add[0].x *= f; add[0].y *= f; add[1].x *= f; add[1].y *= f;
             sum *= f;
@@ -806,33 +840,31 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
         };
         uint32_t s0[32], s1[32];                 // the next 32 columns arrive under the present ones
         tmem_ld32(t_s, s0);
-        tc_wait_ld();
+        tc_wait_ld_of(s0);
 #pragma unroll 1
         for (int c = 0; c < 4; c += 2) {
           tmem_ld32(t_s + c * 32 + 32, s1);
           weigh(s0, c, c ? live.z : live.x);
-          tc_wait_ld();
+          tc_wait_ld_of(s1);
           if (c == 0) tmem_ld32(t_s + 64, s0);
           weigh(s1, c + 1, c ? live.w : live.y);
-          tc_wait_ld();
+          tc_wait_ld_of(s0);
         }
         sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&m->p_full[j]);
+        mbar_arrive(&m->p_full[sb]);
       }
-      // a group without a tile waits for the other's queries here: else it would
-      // arrive for the next piece in this piece's phase
-      if (done == 0) ok = ok && wait_warp(m, &m->q_full, piece & 1u);
       if (!ok) break;
       seq += T;
+      base += steps;
       // ---- the partial rows ----
       const int lr = (x.pair ? j * 128 : 0) + row;
       const int64_t at = x.row + (x.pair ? (int64_t)lr : (int64_t)j * x.rows + lr);
       float4* po = reinterpret_cast<float4*>(p.o + at * D);
       if (done > 0) {
-        if (!(ok = wait_warp(m, &m->o_full[j], no & 1u))) break;
-        ++no;
+        if (!(ok = wait_product(no + done - 1))) break;
+        no += done;
         tc_fence_after();
       }
 #pragma unroll 1
@@ -840,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
         uint32_t o[32];
         if (done > 0) {
           tmem_ld32(t_o + c * 32, o);
-          tc_wait_ld();
+          tc_wait_ld_of(o);
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
