@@ -9,26 +9,42 @@
 // Units of work are (run, kv-head, block of up to 256 rows, tile of 128 key
 // slots = 8 live pages); every CTA of the grid (one per SM) takes an equal
 // contiguous share of them and leaves one partial (reference exponent, sum,
-// unnormalised row) per row and segment it touched, merged by the combine
-// kernel.  Inside a CTA the roles are
-//   warp 17      loads page-head blocks into a byte ring (cp.async.bulk);
+// unnormalised row) per row and segment it touched, merged by merge_kernel
+// (thinkv_decode.cu).  Inside a CTA the roles are
+//   warp 17      loads page-head blocks into a byte ring (cp.async.bulk), a tile
+//                at a time, descriptors and masks requested one and two batches ahead;
 //   warps 8-15   page p of a tile belongs to warp 8 + p: codes and params
 //                become fp16 keys and values, written as the K-major,
 //                128-byte-swizzled operands of tcgen05.mma (values transposed:
 //                the packed V codes pair two tokens of a channel);
-//   warp 16      one thread issues S = Q K^T and O += P V (accumulators and P
-//                in tensor memory);
-//   warps 0-7    two softmax groups, a thread per row: running maximum, P =
-//                2^(s - reference) in fp16, sums in fp32.  The groups alternate, so that
-//                one's exponentials run under the other's products: a block of
-//                more than 128 rows gives each group its own rows, a smaller one
-//                even and odd key tiles.
-// The reference exponent trails the running maximum: P may grow to 2^15 before
-// the accumulators are rescaled, and starts at 2^7, so that the small weights of
-// a long flat row keep fp16's normal precision.
+//   warp 16      issues S = Q K^T and O += P V (accumulators and P in tensor
+//                memory, P over its own scores);
+//   warps 0-7    two softmax groups, a thread per row: P = 2^(s - reference) in
+//                fp16, sums in fp32, one pass over the scores.  The groups
+//                alternate, so that one's exponentials run under the other's products: a
+//                block of more than 128 rows gives each group its own rows, a
+//                smaller one even and odd key tiles.
+// The reference exponent trails the running maximum, by whole numbers: P may
+// grow to 2^15 before the accumulators are rescaled (a power of two, nothing is
+// rounded), and starts at 2^7, so that the small weights of a long flat row keep
+// fp16's normal precision.
 //
-// Rounding: keys, values and P enter the products as fp16 (each value is one
-// fused multiply-add zero + scale * code, rounded once); sums are fp32.
+// Rounding: keys, values and P enter the products as fp16, the widest type that
+// the tensor cores take at full rate beside bf16 (each key or value is one fused
+// multiply-add zero + scale * code, rounded once); everything summed is fp32.
+//
+// 512 rows x 65,536 keys x 8 kv-heads, d = 128, codes of 8, 4 and 2 bits (137
+// GFLOP, 84 us at the measured bf16 rate): 183-205 us.  No unit is busy half the time (issue
+// slots 55 %, products 38 %): what bounds it is each group's chain of scores ->
+// weights -> products, about 5,300 cycles a tile of which 3,000 are softmax; leaving
+// out the exponentials, the unpacking or the products alone takes off 10 to 20 %.
+// Measured on the way: generic instead of shared-space pointers 259 us,
+// operands of the products not warp-uniform (same step), straight-line page writers
+// 350 us and masked softmax code unrolled 611 us (both the instruction cache), pages
+// waited for one by one 403 us, half tiles with two score buffers per group slower (a
+// product of 64 columns costs what one of 128 does), keys written a tile ahead of
+// values no faster, spinning instead of suspended waits no faster.
+
 #include <cuda_fp16.h>
 #include <math.h>
 #include <stdint.h>
