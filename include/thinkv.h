@@ -469,9 +469,12 @@ THINKV_API size_t thinkv_decode_shared_workspace_bytes(const thinkv_layout* L, i
  * every row reads its prefix itself.
  * workspace: device, >= thinkv_decode_shared_workspace_bytes(L, n_seqs, topk)
  * bytes, no initialisation needed; calls that share it must not overlap on the
- * GPU.  Four kernels: the plan (one CTA), the prefix kernel (none of its CTAs
- * has work when no run is worth it; not launched for one row or with
- * topk_mass), then decode's split and combine.  1 <= n_seqs <= 16384. */
+ * GPU.  Four kernels: the plan (one CTA), the prefix kernel (not launched with
+ * topk_mass, nor where even full tables would make it not worth its launch; it
+ * returns at once when no run of the call is), then decode's split and a merge.
+ * Its rows carry fp16 roundings of keys, values and weights (thinkv_prefix.cu's
+ * head), the other rows those of thinkv_decode_attention.
+ * 1 <= n_seqs <= 16384. */
 THINKV_API int thinkv_decode_shared(const thinkv_cache* cache, int32_t n_seqs, const int32_t* seq,
                                     const int32_t* prefix, const uint16_t* q, uint16_t* out,
                                     float* topk_mass, int32_t topk, float softmax_scale,

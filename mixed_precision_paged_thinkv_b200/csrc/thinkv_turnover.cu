@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kApplyWarps * 32, kForkCtas)
         uint4 v[kCopyDepth];
 #pragma unroll
         for (int x = 0; x < kCopyDepth; ++x)
-          if (q + 32 * x < quads) v[x] = __ldg(a + q + 32 * x);
+          if (q + 32 * x < quads) v[x] = __ldcg(a + q + 32 * x);   // (not the read-only path: written by kernels before)
 #pragma unroll
         for (int m = 0; m < kCopies; ++m) {
           if (m >= members) break;
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kApplyWarps * 32, kForkCtas)
           const int64_t pa = __shfl_sync(0xFFFFFFFFu, page, from), pb = __shfl_sync(0xFFFFFFFFu, mine, from);
           if (from < cnt) {
             int32_t* pos = C.slot_pos[pc] + (lane & 15);
-            pos[pb * kPage] = __ldg(pos + pa * kPage);   // (the source's pages change in no fork)
+            pos[pb * kPage] = __ldcg(pos + pa * kPage);
           }
         }
       } else {
