@@ -580,165 +580,165 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
   const uint32_t tmem = m->tmem;
 
   if (warp >= 16) {
-  fewer_regs<kRegsLast>();              // (one instruction for the whole warpgroup)
-  if (warp == kWarpLoad) {
-    // ---------------- loader ----------------
-    // Batches of up to four tiles, a page per lane; the descriptors of a batch are
-    // requested two batches ahead and the live masks one.
-    struct Batch {
-      int64_t row;                            // first entry of the prefix's lists
-      uint64_t desc;
-      uint32_t mask;
-      int h, tiles;
-    };
-    int64_t u = U0, t = 0;
-    Piece x;
-    x.t1 = 0;
-    auto fetch = [&]() {
-      Batch b;
-      b.tiles = 0;
-      b.mask = 0;
-      b.desc = ~0ull;
-      b.row = 0;
-      b.h = 0;
-      if (t >= x.t1) {
-        if (u >= U1) return b;
-        x = piece_at(p, nruns, u, U1, cta);
-        u += x.t1 - x.t0;
-        t = x.t0;
-      }
-      b.row = (int64_t)x.run.prefix * p.max_blocks;
-      b.h = x.h;
-      b.tiles = (int)min((int64_t)4, x.t1 - t);
-      const int64_t j = t * kTilePages + lane;
-      if (lane < b.tiles * kTilePages && j < x.run.pages) b.desc = p.live_list[b.row + j];
-      t += b.tiles;
-      return b;
-    };
-    uint32_t seq = 0, head = 0, used = 0, oldest = 0;   // byte ring, in tiles: [oldest, seq) hold it
-    uint32_t held = 0;                        // lane l < kSlots: ring bytes of the tile in slot l
-    bool ok = true;
-    Batch cur, nxt;
-    cur.tiles = nxt.tiles = 0;
-    nxt.desc = ~0ull;
-    for (int ahead = 2; ok && (ahead > 0 || cur.tiles > 0); --ahead) {
-      if (nxt.desc != ~0ull) nxt.mask = entry_mask(p.table[nxt.row + live_desc_entry(nxt.desc)]);
-      const Batch after = fetch();
-      if (cur.tiles == 0) {                   // the first two rounds only fetch
+    fewer_regs<kRegsLast>();              // (one instruction for the whole warpgroup)
+    if (warp == kWarpLoad) {
+      // ---------------- loader ----------------
+      // Batches of up to four tiles, a page per lane; the descriptors of a batch are
+      // requested two batches ahead and the live masks one.
+      struct Batch {
+        int64_t row;                            // first entry of the prefix's lists
+        uint64_t desc;
+        uint32_t mask;
+        int h, tiles;
+      };
+      int64_t u = U0, t = 0;
+      Piece x;
+      x.t1 = 0;
+      auto fetch = [&]() {
+        Batch b;
+        b.tiles = 0;
+        b.mask = 0;
+        b.desc = ~0ull;
+        b.row = 0;
+        b.h = 0;
+        if (t >= x.t1) {
+          if (u >= U1) return b;
+          x = piece_at(p, nruns, u, U1, cta);
+          u += x.t1 - x.t0;
+          t = x.t0;
+        }
+        b.row = (int64_t)x.run.prefix * p.max_blocks;
+        b.h = x.h;
+        b.tiles = (int)min((int64_t)4, x.t1 - t);
+        const int64_t j = t * kTilePages + lane;
+        if (lane < b.tiles * kTilePages && j < x.run.pages) b.desc = p.live_list[b.row + j];
+        t += b.tiles;
+        return b;
+      };
+      uint32_t seq = 0, head = 0, used = 0, oldest = 0;   // byte ring, in tiles: [oldest, seq) hold it
+      uint32_t held = 0;                        // lane l < kSlots: ring bytes of the tile in slot l
+      bool ok = true;
+      Batch cur, nxt;
+      cur.tiles = nxt.tiles = 0;
+      nxt.desc = ~0ull;
+      for (int ahead = 2; ok && (ahead > 0 || cur.tiles > 0); --ahead) {
+        if (nxt.desc != ~0ull) nxt.mask = entry_mask(p.table[nxt.row + live_desc_entry(nxt.desc)]);
+        const Batch after = fetch();
+        if (cur.tiles == 0) {                   // the first two rounds only fetch
+          cur = nxt;
+          nxt = after;
+          continue;
+        }
+        const bool page = cur.desc != ~0ull;
+        const int c = page ? entry_class(cur.desc) : 0;
+        const uint32_t bytes = page ? (uint32_t)p.phb[c] : 0u;
+        const uint64_t src = reinterpret_cast<uint64_t>(p.pool[c]) +
+                             ((uint64_t)entry_page(cur.desc) * p.Hkv + cur.h) * (uint64_t)p.phb[c];
+        uint32_t end = bytes;                   // prefix sums inside each tile's eight lanes
+#pragma unroll
+        for (int o = 1; o < kTilePages; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, end, o);
+          if ((lane & 7) >= o) end += y;
+        }
+        for (int k = 0; k < cur.tiles; ++k, ++seq) {
+          const uint32_t total = __shfl_sync(0xFFFFFFFFu, end, 8 * k + 7), slot = seq % kSlots;
+          uint32_t pad;
+          bool wrap;
+          while (true) {                        // until the slot and enough bytes have been given back
+            if (used == 0) head = 0;
+            wrap = head + total > (uint32_t)S::ring;
+            pad = wrap ? (uint32_t)S::ring - head : 0u;
+            if (seq - oldest < (uint32_t)kSlots && used + pad + total <= (uint32_t)S::ring) break;
+            if (!(ok = wait_warp(m, &m->raw_empty[oldest % kSlots], (oldest / kSlots) & 1u))) break;
+            used -= __shfl_sync(0xFFFFFFFFu, held, oldest % kSlots);
+            ++oldest;
+          }
+          if (!ok) break;
+          if (wrap) head = 0;
+          const uint32_t at = head + end - bytes;
+          if ((lane >> 3) == k) {
+            m->slot_off[slot][lane & 7] = at;
+            m->slot_bits[slot][lane & 7] = page ? ((uint32_t)p.bits[c] | (cur.mask << 16)) : 0u;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&m->raw_full[slot], total);
+          __syncwarp();
+          if ((lane >> 3) == k && page)
+            bulk_g2s(smem + S::off_ring + at, reinterpret_cast<const void*>(src), bytes, &m->raw_full[slot]);
+          if (lane == (int)slot) held = pad + total;
+          head += total;
+          used += pad + total;
+        }
         cur = nxt;
         nxt = after;
-        continue;
       }
-      const bool page = cur.desc != ~0ull;
-      const int c = page ? entry_class(cur.desc) : 0;
-      const uint32_t bytes = page ? (uint32_t)p.phb[c] : 0u;
-      const uint64_t src = reinterpret_cast<uint64_t>(p.pool[c]) +
-                           ((uint64_t)entry_page(cur.desc) * p.Hkv + cur.h) * (uint64_t)p.phb[c];
-      uint32_t end = bytes;                   // prefix sums inside each tile's eight lanes
-#pragma unroll
-      for (int o = 1; o < kTilePages; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, end, o);
-        if ((lane & 7) >= o) end += y;
-      }
-      for (int k = 0; k < cur.tiles; ++k, ++seq) {
-        const uint32_t total = __shfl_sync(0xFFFFFFFFu, end, 8 * k + 7), slot = seq % kSlots;
-        uint32_t pad;
-        bool wrap;
-        while (true) {                        // until the slot and enough bytes have been given back
-          if (used == 0) head = 0;
-          wrap = head + total > (uint32_t)S::ring;
-          pad = wrap ? (uint32_t)S::ring - head : 0u;
-          if (seq - oldest < (uint32_t)kSlots && used + pad + total <= (uint32_t)S::ring) break;
-          if (!(ok = wait_warp(m, &m->raw_empty[oldest % kSlots], (oldest / kSlots) & 1u))) break;
-          used -= __shfl_sync(0xFFFFFFFFu, held, oldest % kSlots);
-          ++oldest;
-        }
-        if (!ok) break;
-        if (wrap) head = 0;
-        const uint32_t at = head + end - bytes;
-        if ((lane >> 3) == k) {
-          m->slot_off[slot][lane & 7] = at;
-          m->slot_bits[slot][lane & 7] = page ? ((uint32_t)p.bits[c] | (cur.mask << 16)) : 0u;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&m->raw_full[slot], total);
-        __syncwarp();
-        if ((lane >> 3) == k && page)
-          bulk_g2s(smem + S::off_ring + at, reinterpret_cast<const void*>(src), bytes, &m->raw_full[slot]);
-        if (lane == (int)slot) held = pad + total;
-        head += total;
-        used += pad + total;
-      }
-      cur = nxt;
-      nxt = after;
-    }
-    // every block in flight has landed before the CTA ends
-    if (lane == 0)
-      for (uint32_t y = seq > kSlots ? seq - kSlots : 0; y < seq; ++y)
-        mbar_wait_bounded(&m->raw_full[y % kSlots], (y / kSlots) & 1u);
-  } else if (warp == kWarpMma) {
-    // ---------------- products ----------------
-    // The whole warp keeps the books, so that the operands are warp-uniform; one
-    // lane issues.
-    const uint32_t lead = elect_one();
-    uint32_t seq = 0, piece = 0, base = 0;           // tiles, pieces, steps before this piece
-    uint32_t odd = 0;                                // bit j: group j's next product has an odd number
-    const uint64_t q_desc = operand_desc(smem_u32(smem + S::off_q)), kv_desc = operand_desc(smem_u32(smem + S::off_kv));
-    bool ok = true;
-    for (int64_t u = U0; ok && u < U1; ++piece) {
-      const Piece x = piece_at(p, nruns, u, U1, cta);
-      u += x.t1 - x.t0;
-      const uint32_t T = __shfl_sync(0xFFFFFFFFu, (uint32_t)(x.t1 - x.t0), 0);
-      const uint32_t pair = __shfl_sync(0xFFFFFFFFu, (uint32_t)x.pair, 0);
-      const uint32_t steps = T << pair;              // products of one group and one key tile
-      ok = wait_warp(m, &m->q_full, piece & 1u);
-      constexpr uint32_t NS = S::s_bufs;             // scores are made NS steps ahead of the values
-      for (uint32_t s = 0; ok && s < steps + NS; ++s) {
-        if (s >= NS) {                               // O_j += P_j V
-          const uint32_t r = s - NS, j = r & 1u, pos = 2 * (seq + (r >> pair)) + 1, buf = pos % S::kv_bufs;
-          const uint32_t g = base + r, sb = g % NS;
-          if (!pair || j == 0) ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
-          ok = ok && wait_warp(m, &m->p_full[sb], (g / NS) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t b = kv_desc + buf * (S::kv_bytes >> 4);
-          const uint32_t d = tmem + S::col_o + j * D, a = tmem + sb * kTile;
-          if (lead) {
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_ts(d, a + k * 8, b + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), instr_desc(D), r >= 2 || k > 0);
-            if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
-            mma_commit(&m->o_done[j][(odd >> j) & 1u]);
-          }
-          odd ^= 1u << j;
-          __syncwarp();
-        }
-        if (s < steps) {                             // S_j = Q_j K^T
-          const uint32_t j = s & 1u, pos = 2 * (seq + (s >> pair)), buf = pos % S::kv_bufs;
-          const uint32_t sb = (base + s) % NS;
-          if (!pair || j == 0) {
-            ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
+      // every block in flight has landed before the CTA ends
+      if (lane == 0)
+        for (uint32_t y = seq > kSlots ? seq - kSlots : 0; y < seq; ++y)
+          mbar_wait_bounded(&m->raw_full[y % kSlots], (y / kSlots) & 1u);
+    } else if (warp == kWarpMma) {
+      // ---------------- products ----------------
+      // The whole warp keeps the books, so that the operands are warp-uniform; one
+      // lane issues.
+      const uint32_t lead = elect_one();
+      uint32_t seq = 0, piece = 0, base = 0;           // tiles, pieces, steps before this piece
+      uint32_t odd = 0;                                // bit j: group j's next product has an odd number
+      const uint64_t q_desc = operand_desc(smem_u32(smem + S::off_q)), kv_desc = operand_desc(smem_u32(smem + S::off_kv));
+      bool ok = true;
+      for (int64_t u = U0; ok && u < U1; ++piece) {
+        const Piece x = piece_at(p, nruns, u, U1, cta);
+        u += x.t1 - x.t0;
+        const uint32_t T = __shfl_sync(0xFFFFFFFFu, (uint32_t)(x.t1 - x.t0), 0);
+        const uint32_t pair = __shfl_sync(0xFFFFFFFFu, (uint32_t)x.pair, 0);
+        const uint32_t steps = T << pair;              // products of one group and one key tile
+        ok = wait_warp(m, &m->q_full, piece & 1u);
+        constexpr uint32_t NS = S::s_bufs;             // scores are made NS steps ahead of the values
+        for (uint32_t s = 0; ok && s < steps + NS; ++s) {
+          if (s >= NS) {                               // O_j += P_j V
+            const uint32_t r = s - NS, j = r & 1u, pos = 2 * (seq + (r >> pair)) + 1, buf = pos % S::kv_bufs;
+            const uint32_t g = base + r, sb = g % NS;
+            if (!pair || j == 0) ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
+            ok = ok && wait_warp(m, &m->p_full[sb], (g / NS) & 1u);
             if (!ok) break;
-          }
-          tc_fence_after();
-          const uint64_t a = q_desc + (pair ? j : 0u) * (S::q_bytes >> 4), b = kv_desc + buf * (S::kv_bytes >> 4);
-          const uint32_t d = tmem + sb * kTile;
-          if (lead) {
+            tc_fence_after();
+            const uint64_t b = kv_desc + buf * (S::kv_bytes >> 4);
+            const uint32_t d = tmem + S::col_o + j * D, a = tmem + sb * kTile;
+            if (lead) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
-              mma_ss(d, a + off, b + off, instr_desc(kTile), k > 0);
+              for (int k = 0; k < kTile / 16; ++k)
+                mma_ts(d, a + k * 8, b + (((k / 4) * (D * 128) + (k % 4) * 32) >> 4), instr_desc(D), r >= 2 || k > 0);
+              if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
+              mma_commit(&m->o_done[j][(odd >> j) & 1u]);
             }
-            mma_commit(&m->s_full[sb]);
-            if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
+            odd ^= 1u << j;
+            __syncwarp();
           }
-          __syncwarp();
+          if (s < steps) {                             // S_j = Q_j K^T
+            const uint32_t j = s & 1u, pos = 2 * (seq + (s >> pair)), buf = pos % S::kv_bufs;
+            const uint32_t sb = (base + s) % NS;
+            if (!pair || j == 0) {
+              ok = wait_warp(m, &m->kv_full[buf], (pos / S::kv_bufs) & 1u);
+              if (!ok) break;
+            }
+            tc_fence_after();
+            const uint64_t a = q_desc + (pair ? j : 0u) * (S::q_bytes >> 4), b = kv_desc + buf * (S::kv_bytes >> 4);
+            const uint32_t d = tmem + sb * kTile;
+            if (lead) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+                mma_ss(d, a + off, b + off, instr_desc(kTile), k > 0);
+              }
+              mma_commit(&m->s_full[sb]);
+              if (!pair || j == 1) mma_commit(&m->kv_empty[buf]);
+            }
+            __syncwarp();
+          }
         }
+        base += steps;
+        seq += T;
       }
-      base += steps;
-      seq += T;
     }
-  }
   } else if (warp >= 8) {
     fewer_regs<kRegsDequant>();
     // ---------------- codes -> fp16 operands ----------------
