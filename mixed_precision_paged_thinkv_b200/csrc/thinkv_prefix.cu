@@ -842,6 +842,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
           if (__any_sync(0xFFFFFFFFu, mx > ref + kSlack)) {
             const float to = mx > ref + kSlack ? ceilf(mx) : ref;
             const float f = ref > -INFINITY ? exp2_approx(ref - to) : (to > -INFINITY ? 0.f : 1.f);
+            // what is scaled here was stored by this thread (weights of earlier columns,
+            // accumulators of an earlier move): a load is not ordered behind such a store
+            tc_wait_st();
             if (done > 0) {                      // the group's last product may still be running
               ok = ok && wait_product(no + done - 1);
               tc_fence_after();
