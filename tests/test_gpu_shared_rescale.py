@@ -82,3 +82,22 @@ def test_maximum_jumps_in_every_quarter_of_a_tile(heads, members):
     v = torch.randn(n, h, d, generator=gen)
     c = _raw_cache(heads, k, v, members)
     _check(c, k, v, _queries(heads, members, 1), members)
+
+
+@pytest.mark.parametrize("quarter", [0, 1, 2, 3])
+@pytest.mark.parametrize("heads,members", [("gqa4", 64), ("gqa8", 15)])
+def test_maximum_jumps_once_a_tile(heads, members, quarter):
+    """One move a tile, in each of its quarters: the weights stored before it, up to
+    96 keys a few powers of two below the new maximum, still carry a share of the row."""
+    hq, h, d, g = HEADS[heads]
+    n = 100 * TILE + 37
+    gen = torch.Generator().manual_seed(quarter)
+    k = torch.zeros(n, h, d)
+    at = torch.arange(n) + (4 - quarter) * 32             # the score rises where this reaches the next tile
+    k[:, :, 0] = (10.0 * (at // TILE))[:, None]
+    k[:, :, 1] = torch.randint(-1, 2, (n, h), generator=gen).float()
+    v = torch.randn(n, h, d, generator=gen)
+    # what lies before a move is large, so that it is seen under what follows
+    v[at % TILE >= 64] *= 64
+    c = _raw_cache(heads, k, v, members)
+    _check(c, k, v, _queries(heads, members, 2), members)
