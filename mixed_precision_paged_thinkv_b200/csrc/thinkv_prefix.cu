@@ -25,9 +25,11 @@
 //                block of more than 128 rows gives each group its own rows, a
 //                smaller one even and odd key tiles.
 // The reference exponent trails the running maximum, by whole numbers: P may
-// grow to 2^15 before the accumulators are rescaled (a power of two, nothing is
-// rounded), and starts at 2^7, so that the small weights of a long flat row keep
-// fp16's normal precision.
+// grow to 2^15 before it is rescaled by a power of two, and starts at 2^7, so that
+// the small weights of a long flat row keep fp16's normal precision.  A rescale
+// is exact for the fp32 sums and accumulators; weights of the same tile that are
+// already stored as fp16 lose what falls below 2^-24, as if weighed under the new
+// reference at once: 2^-25 each beside a largest weight of 2^6 or more.
 //
 // Rounding: keys, values and P enter the products as fp16, the widest type that
 // the tensor cores take at full rate beside bf16 (each key or value is one fused
@@ -488,14 +490,17 @@ __device__ __forceinline__ void scale_columns(uint32_t addr, float f) {
     tmem_st32(addr + c * 32, o);
   }
 }
-// 32 weights (fp16, 16 columns) of this thread's row, times f
+// 32 weights (fp16, 16 columns) of this thread's row, times f.  In fp32: as an fp16
+// factor f would be 0 from 2^-25 on, where weights of up to 2^15 are not.
 __device__ __forceinline__ void scale_weights(uint32_t addr, float f) {
   uint32_t w[16];
   tmem_ld16(addr, w);
   tc_wait_ld_of(w);
-  const __half2 h = __float2half2_rn(f);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) w[e] = as_bits(__hmul2(as_half2(w[e]), h));
+  for (int e = 0; e < 16; ++e) {
+    const float2 v = __half22float2(as_half2(w[e]));
+    w[e] = pack_half2_rn(v.x * f, v.y * f);
+  }
   tmem_st16(addr, w);
 }
 
@@ -844,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_kernel(PrefixParams p) {
           if (!full) hide_dead(sc, live_c);
           const float mx = max32(sc) * p.scale_log2 - kHeadroom;
           // a row whose maximum has outgrown its reference moves it, and what
-          // was summed under it: a whole power of two, so nothing is rounded
+          // was weighed and summed under it, by a whole power of two
           if (__any_sync(0xFFFFFFFFu, mx > ref + kSlack)) {
             const float to = mx > ref + kSlack ? ceilf(mx) : ref;
             const float f = ref > -INFINITY ? exp2_approx(ref - to) : (to > -INFINITY ? 0.f : 1.f);

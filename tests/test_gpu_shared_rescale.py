@@ -101,3 +101,23 @@ def test_maximum_jumps_once_a_tile(heads, members, quarter):
     v[at % TILE >= 64] *= 64
     c = _raw_cache(heads, k, v, members)
     _check(c, k, v, _queries(heads, members, 2), members)
+
+
+@pytest.mark.parametrize("jump", [12.0, 17.5, 20.0])
+@pytest.mark.parametrize("heads,members", [("gqa4", 64), ("gqa8", 15)])
+def test_weights_before_a_large_jump_count(heads, members, jump):
+    """64 keys eight powers of two above the first ones (they stay under the same
+    reference), then keys far above them in the same tile, whose values are zero: the
+    output is what is left of the 64 keys' weights, to fp16's relative precision."""
+    hq, h, d, g = HEADS[heads]
+    n = 100 * TILE
+    gen = torch.Generator().manual_seed(3)
+    k = torch.zeros(n, h, d)
+    k[:, :, 0] = -100.0
+    k[:32, :, 0], k[32:96, :, 0], k[96:128, :, 0] = 0.0, 8.0, 8.0 + jump
+    v = torch.zeros(n, h, d)
+    v[32:96] = 500 + 500 * torch.rand(64, h, d, generator=gen)
+    c = _raw_cache(heads, k, v, members)
+    q = torch.zeros(members, hq, d)
+    q[:, :, 0] = 1.0
+    _check(c, k, v, q.half().cuda(), members)
