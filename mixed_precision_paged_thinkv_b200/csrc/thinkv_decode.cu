@@ -724,8 +724,10 @@ __device__ inline void page_step(SegState<D, G>& S, const uint8_t* blk, uint32_t
     for (int gr = 0; gr < NG; ++gr) {
       const int ef0 = (__float_as_int(s0[gr]) >> 23) - 112;   // fp16 exponent field
       const int ef1 = (__float_as_int(s1[gr]) >> 23) - 112;
-      e5 = live0 ? max(e5, ef0) : e5;
-      e5 = live1 ? max(e5, ef1) : e5;
+      // (a scale that is not finite, field 31 as fp16, makes its own group not finite;
+      // sigma would take the other groups' weights to 0 with it)
+      e5 = live0 && ef0 < 31 ? max(e5, ef0) : e5;
+      e5 = live1 && ef1 < 31 ? max(e5, ef1) : e5;
     }
     // over the page's 16 tokens: the lanes of other g hold the other tokens
     e5 = max(e5, __shfl_xor_sync(0xFFFFFFFFu, e5, 4));
