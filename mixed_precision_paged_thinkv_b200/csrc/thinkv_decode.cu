@@ -688,9 +688,10 @@ __device__ inline void page_step(SegState<D, G>& S, const uint8_t* blk, uint32_t
       const float2 sz1 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
       s0[gr] = sz0.x;
       s1[gr] = sz1.x;
-      constexpr float voff = F == 1 ? 0.f : (float)(1 << (B - 1));
-      const float zv0 = live0 ? fmaf(voff, sz0.x, sz0.y) : 0.f;
-      const float zv1 = live1 ? fmaf(voff, sz1.x, sz1.y) : 0.f;
+      // (float codes have no offset: not 0 * scale, which an infinite scale makes a NaN)
+      constexpr float voff = (float)(1 << (B - 1));
+      const float zv0 = live0 ? (F == 1 ? sz0.y : fmaf(voff, sz0.x, sz0.y)) : 0.f;
+      const float zv1 = live1 ? (F == 1 ? sz1.y : fmaf(voff, sz1.x, sz1.y)) : 0.f;
       S.z[gr][0] = fmaf(S.z[gr][0], a0, fmaf(pr[0], zv0, pr[2] * zv1));
       S.z[gr][1] = fmaf(S.z[gr][1], a1, fmaf(pr[1], zv0, pr[3] * zv1));
     }

@@ -65,7 +65,8 @@ def _reference(c, seq, q):
 
 WHERE = pytest.mark.parametrize("heads,bits,tag", [
     ("gqa4", "842", 0), ("gqa4", "842", 1), ("gqa4", "842", 2), ("gqa8", "842", 1), ("gqa4", "float", 0),
-    ("gqa4", "float", 2), ("mha", "two", 1), ("gqa4", "raws", 0), ("gqa8", "raws", 2)])
+    ("gqa4", "float", 1), ("gqa4", "float", 2), ("mha", "two", 1), ("gqa8", "fp4", 0), ("gqa4", "raws", 0),
+    ("gqa8", "raws", 2)])
 
 
 @pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
