@@ -263,16 +263,20 @@ template <int B, int F>
 __device__ constexpr float largest_code() {
   return F == 1 ? (B == 8 ? 448.f : B == 4 ? 6.f : 2.f) : (float)((1 << B) - 1);   // (ternary codes: 0..2)
 }
-// A scale whose largest value zero + scale * code would round past fp16's range
-// (past 65504 + 16, which would become inf) is lowered to what fits.
+// A finite scale whose largest value zero + scale * code would round past fp16's
+// range (from 65504 + 16 on, which would become inf) is lowered to what fits.  A
+// scale or zero that is infinite or not a number stays what it is, and so does
+// the other scale of a pair.
 template <int B, int F>
 __device__ __forceinline__ __half2 fitting(__half2 s, __half2 z) {
   const __half2 top = __hfma2(s, __float2half2_rn(largest_code<B, F>()), z);
   if (!__hble2(top, __float2half2_rn(65504.f))) {
-    const float2 zf = __half22float2(z), sf = __half22float2(s);
-    const float k = 1.f / largest_code<B, F>();
-    s = __halves2half2(__float2half_rd(fminf(sf.x, (65504.f - zf.x) * k)),
-                       __float2half_rd(fminf(sf.y, (65504.f - zf.y) * k)));
+    auto fit = [](__half sh, __half zh) {
+      const float sf = __half2float(sh), zf = __half2float(zh);
+      const float t = fmaf(sf, largest_code<B, F>(), zf);
+      return t >= 65520.f && t < INFINITY ? __float2half_rd((65504.f - zf) / largest_code<B, F>()) : sh;
+    };
+    s = __halves2half2(fit(__low2half(s), __low2half(z)), fit(__high2half(s), __high2half(z)));
   }
   return s;
 }

@@ -1,5 +1,5 @@
 """Shared-prefix decode over live tokens that hold an infinity or a NaN: the
-split kernel answers what the definition says (zero + code *
+prefix kernel and the split kernel answer what the definition says (zero + code *
 scale, softmax over all tokens), not-a-numbers and infinities included, and the
 heads without such a token stay as exact as ever."""
 import numpy as np
@@ -89,3 +89,18 @@ def test_rows_alone(heads, bits, tag, kv, value):
     torch.cuda.synchronize()
     assert c.status() == 0
     _same(out, ref, bound, "decode")
+
+
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("kv", [0, 1])
+@WHERE
+def test_rows_of_a_run(heads, bits, tag, kv, value):
+    """The prefix kernel: rows that read the prefix together."""
+    c, seq = _cache(heads, bits, tag, kv, value)
+    assert (MEMBERS - 1) * c.snapshot()["num_live"][0] * c.H >= 8192
+    q = np.random.default_rng(4).standard_normal((MEMBERS, c.Hq, c.d)).astype(np.float16)
+    ref, bound = _reference(c, seq, q)
+    out = c.decode_shared(_ids(seq), _ids([0] * MEMBERS), torch.from_numpy(q).cuda())[0]
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    _same(out, ref, bound, "rows of a run")
