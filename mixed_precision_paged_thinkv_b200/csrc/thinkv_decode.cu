@@ -29,6 +29,7 @@
 //   head sorting and merging the pieces' top-k candidates -- and writes fp16 O
 //   and the top-k mass.
 #include <cuda_fp16.h>
+#include <float.h>
 #include <limits.h>
 #include <mutex>
 #include <stdint.h>
@@ -372,7 +373,8 @@ __device__ inline void seg_begin(SegState<D, G>& S, const DecodeParams& p, const
     S.z[gr][0] = S.z[gr][1] = 0.f;
   }
   S.sigma = kSigmaInit;               // the first page sets sigma
-  S.m[0] = S.m[1] = -INFINITY;
+  // (finite: a page whose scores are all -inf leaves it there, and weighs 0 under it)
+  S.m[0] = S.m[1] = -FLT_MAX;
   S.lp[0] = S.lp[1] = 0.f;
   S.th[0] = S.th[1] = -INFINITY;
 #pragma unroll

@@ -104,3 +104,38 @@ def test_rows_of_a_run(heads, bits, tag, kv, value):
     torch.cuda.synchronize()
     assert c.status() == 0
     _same(out, ref, bound, "rows of a run")
+
+
+@pytest.mark.parametrize("heads", ["gqa4", "gqa8"])
+@pytest.mark.parametrize("bad", [16, 700])
+def test_keys_without_weight(heads, bad):
+    """Whole pages and tiles of raw keys whose scores are -inf, first in the list: a
+    row's maximum is -inf until its first finite score, and their weight is 0."""
+    hq, h, d, g = HEADS[heads]
+    c = ThinKVCache(hq, h, d, g, (16, 16, 16), MEMBERS + 1, 200, (300, 1, 1))
+    gen = torch.Generator().manual_seed(bad)
+    x = torch.randn(2, TOKENS, h, d, generator=gen).half()
+    x[0, :bad, :, 5] = np.inf
+    x = x.cuda()
+    c.append(_ids([0] * TOKENS), _ids(range(TOKENS)), torch.zeros(TOKENS, dtype=torch.uint8, device="cuda"), x[0], x[1])
+    seq = list(range(1, MEMBERS + 1))
+    q = np.random.default_rng(bad).standard_normal((MEMBERS, hq, d)).astype(np.float16)
+    q[:, :, 5] = -np.abs(q[:, :, 5]) - np.float16(0.1)
+    qd = torch.from_numpy(q).cuda()
+    exact = Exact(c)
+    exact.kept[0] = [y[bad:] for y in exact.tokens(0)]
+    ref, _, bound = exact.rows(seq, [0] * MEMBERS, q)
+    run = c.decode_shared(_ids(seq), _ids([0] * MEMBERS), qd)[0]
+    alone = torch.cat([c.decode_shared(_ids([1]), _ids([0]), qd[i:i + 1])[0] for i in range(6)])
+    one = torch.cat([c.decode(_ids([0]), qd[i:i + 1])[0] for i in range(6)])
+    many = c.decode(_ids([0] * MEMBERS), qd)[0]
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    _same(run, ref, bound, "rows of a run")
+    _same(alone, ref[:6], bound[:6], "rows alone")
+    _same(one, ref[:6], bound[:6], "decode")
+    _same(many, ref, bound, "decode of many rows")
+    with np.errstate(invalid="ignore"):
+        odd, _, _ = Exact(c).rows([1], [0], -q[:1])      # scores of +inf
+    out = c.decode_shared(_ids([1]), _ids([0]), -qd[:1])[0]
+    assert np.isnan(odd).all() and torch.isnan(out).all()
