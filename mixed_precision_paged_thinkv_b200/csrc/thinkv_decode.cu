@@ -1078,36 +1078,8 @@ constexpr int kCombinePieces = 128;             // pieces per round of the weigh
 // piece's top-k candidates for head r and merges their largest into a running
 // list (bitonic networks, the next piece's candidates loaded while the current
 // ones are sorted) for the top-k mass.
-// A row's pieces from the prefix kernel: the CTAs of its grid that hold units of
-// the row's segment, two partials each where the block has at most 128 rows.
-struct PrefixPieces {
-  int64_t units, first_unit, first_cta, base;
-  int count, halves, half_rows;
-  bool by_unit;
-  __device__ void find(const DecodeParams& p, int i, int h, int r) {
-    const SharedRun run = p.plan.run[r];
-    const RunShape s = run_shape(run.count, run.pages, p.Gq);
-    const int b = (i - run.first) / s.members, in_block = (i - run.first) - b * s.members;
-    half_rows = min(s.members, run.count - b * s.members) * p.Gq;
-    halves = half_rows > 128 ? 1 : 2;
-    units = p.plan.rstart[*p.plan.nruns];
-    first_unit = p.plan.rstart[r] + ((int64_t)h * s.blocks + b) * s.tiles;
-    by_unit = units <= p.prefix_grid;
-    first_cta = warp_of_unit(first_unit, units, p.prefix_grid);
-    const int64_t last = warp_of_unit(first_unit + s.tiles - 1, units, p.prefix_grid);
-    count = halves * (int)(by_unit ? s.tiles : last - first_cta + 1);
-    base = partial_row(run, s, p.Hkv, p.Gq, h, b, 0) + (int64_t)in_block * p.Gq;
-  }
-  // row of piece x for the first of the kv-head's query heads
-  __device__ int64_t row(const DecodeParams& p, int x) const {
-    const int j = halves == 2 ? x >> 1 : x;
-    const int64_t c = by_unit ? warp_of_unit(first_unit + j, units, p.prefix_grid) : first_cta + j;
-    return base + c * kBlockRows + (halves == 2 && (x & 1) ? half_rows : 0);
-  }
-};
-
-// SHARED: the partial rows that the prefix kernel left for the row follow the
-// split kernel's records in the list of pieces.
+// SHARED (only with the top-k statistic, whose rows the split kernel reads whole):
+// the plan has the prefix sums; calls without it take merge_kernel.
 template <int D, bool TOPK, bool SHARED>
 __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_kernel(DecodeParams p) {
   constexpr int QD = D / 4;
@@ -1122,26 +1094,13 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   if constexpr (SHARED) pref = p.plan.pref;
   else pref = p.pref;
   const int nl = (int)(pref[i + 1] - pref[i]);
-  if (!SHARED && nl == 0) return;               // written by the split kernel
+  if (nl == 0) return;                          // written by the split kernel
   const int64_t T = (int64_t)pref[p.n] * p.Hkv, W = sharing_warps<SHARED>((int64_t)pref[p.n] * p.Hkv, p.split_warps);
   const int64_t Us = (int64_t)pref[i] * p.Hkv + (int64_t)h * nl, Ue = Us + nl;
-  const bool any = !SHARED || nl > 0;
-  const int64_t w0 = any ? warp_of_unit(Us, T, W) : 0, w1 = any ? warp_of_unit(Ue - 1, T, W) : 0;
+  const int64_t w0 = warp_of_unit(Us, T, W), w1 = warp_of_unit(Ue - 1, T, W);
   const bool by_unit = T <= W;                  // one unit per warp
-  const int np_split = any ? (int)(by_unit ? nl : w1 - w0 + 1) : 0;
-  int np = np_split;
-  PrefixPieces pp;                              // of the prefix kernel (SHARED)
-  if constexpr (SHARED) {
-    const int r = p.plan.item[i].w;
-    if (r >= 0) {
-      pp.find(p, i, h, r);
-      np += pp.count;
-    } else if (np <= 1) {
-      return;
-    }
-  } else {
-    if (np <= 1) return;                        // finished inside one split warp
-  }
+  const int np = (int)(by_unit ? nl : w1 - w0 + 1);
+  if (np <= 1) return;                          // finished inside one split warp
   const int Gq = p.Gq, k = p.topk;
   // the top-k warps' live count, requested now and used after the merge
   const pages_t<SHARED> live_i = (p.mass && threadIdx.x < 32 * Gq) ? live_tokens<SHARED>(p, i) : 0;
@@ -1167,13 +1126,10 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   const int r_o = tid / QD, q_o = tid - (tid / QD) * QD;
   const bool out_thread = tid < Gq * QD;
   auto quad = [&](int j) {
-    if (SHARED && j >= np_split)
-      return __ldcg(reinterpret_cast<const float4*>(p.prefix_o + (pp.row(p, j - np_split) + r_o) * D) + q_o);
     return __ldcg(reinterpret_cast<const float4*>(rec(j) + 64) + r_o * QD + q_o);
   };
   auto pair_ml = [&](int x) {
     const int j = x / Gq, r = x - j * Gq;
-    if (SHARED && j >= np_split) return __ldcg(p.prefix_ml + pp.row(p, j - np_split) + r);
     return __ldcg(reinterpret_cast<const float2*>(rec(j)) + r);
   };
   // the first pieces' quads and (m, l) pairs do not depend on the weights:
@@ -1381,6 +1337,34 @@ __global__ void __launch_bounds__(kCombineThreads, TOPK ? 4 : 3) decode_combine_
   if (lane == 0) p.mass[mrow] = sum / sL[r];
 }
 
+// A row's pieces from the prefix kernel: the CTAs of its grid that hold units of
+// the row's segment, two partials each where the block has at most 128 rows.
+struct PrefixPieces {
+  int64_t units, first_unit, first_cta, base;
+  int count, halves, half_rows;
+  bool by_unit;
+  __device__ void find(const DecodeParams& p, int i, int h, int r) {
+    const SharedRun run = p.plan.run[r];
+    const RunShape s = run_shape(run.count, run.pages, p.Gq);
+    const int b = (i - run.first) / s.members, in_block = (i - run.first) - b * s.members;
+    half_rows = min(s.members, run.count - b * s.members) * p.Gq;
+    halves = half_rows > 128 ? 1 : 2;
+    units = p.plan.rstart[*p.plan.nruns];
+    first_unit = p.plan.rstart[r] + ((int64_t)h * s.blocks + b) * s.tiles;
+    by_unit = units <= p.prefix_grid;
+    first_cta = warp_of_unit(first_unit, units, p.prefix_grid);
+    const int64_t last = warp_of_unit(first_unit + s.tiles - 1, units, p.prefix_grid);
+    count = halves * (int)(by_unit ? s.tiles : last - first_cta + 1);
+    base = partial_row(run, s, p.Hkv, p.Gq, h, b, 0) + (int64_t)in_block * p.Gq;
+  }
+  // row of piece x for the first of the kv-head's query heads
+  __device__ int64_t row(const DecodeParams& p, int x) const {
+    const int j = halves == 2 ? x >> 1 : x;
+    const int64_t c = by_unit ? warp_of_unit(first_unit + j, units, p.prefix_grid) : first_cta + j;
+    return base + c * kBlockRows + (halves == 2 && (x & 1) ? half_rows : 0);
+  }
+};
+
 // The combine of a SHARED call without the top-k statistic: a CTA per (sequence,
 // kv-head), whose pieces are the split kernel's records and the prefix kernel's
 // partial rows.  Groups of Gq * D/4 threads (a quad of one head's row each) take
@@ -1502,22 +1486,22 @@ cudaError_t launch_split_t(const DecodeParams& p, const DecodeLaunch& dl, cudaSt
   e = launch_pdl(decode_split_kernel<D, G, TOPK, SHARED>, dim3(dl.grid), dim3(SplitShape<D>::threads), dl.smem_bytes,
                  stream, p);
   if (e != cudaSuccess) return e;
-  if constexpr (SHARED && !TOPK)
-  {
+  if constexpr (SHARED && !TOPK) {
     // four groups of Gq * D/4 threads, at least a warp a head
     int mt = (4 * p.Gq * (D / 4) + 31) / 32 * 32;
     if (mt < 32 * p.Gq) mt = 32 * p.Gq;
     if (mt < 128) mt = 128;
     if (mt > kMergeThreads) mt = kMergeThreads;
     return launch_pdl(merge_kernel<D>, dim3((unsigned)(p.n * p.Hkv)), dim3(mt), 0, stream, p);
+  } else {
+    // the combine: one CTA per segment (most return at once), as many threads as
+    // the segment's output quads (Gq * D/4), and a warp per head at least (the
+    // per-head sums, the top-k merges)
+    const int qt = (p.Gq * (D / 4) + 31) / 32 * 32;
+    const int ct = qt > 32 * p.Gq ? qt : 32 * p.Gq;
+    return launch_pdl(decode_combine_kernel<D, TOPK, SHARED>, dim3((unsigned)(p.n * p.Hkv)),
+                      dim3(ct < kCombineThreads ? ct : kCombineThreads), 0, stream, p);
   }
-  // the combine: one CTA per segment (most return at once), as many threads as
-  // the segment's output quads (Gq * D/4), and a warp per head at least (the
-  // per-head sums, the top-k merges)
-  const int qt = (p.Gq * (D / 4) + 31) / 32 * 32;
-  const int ct = qt > 32 * p.Gq ? qt : 32 * p.Gq;
-  return launch_pdl(decode_combine_kernel<D, TOPK, SHARED>, dim3((unsigned)(p.n * p.Hkv)),
-                    dim3(ct < kCombineThreads ? ct : kCombineThreads), 0, stream, p);
 }
 
 // the top-k candidate code is compiled only into the instantiation that uses it
