@@ -225,7 +225,7 @@ class ThinKVCache:
             self.cs.slot_pos[c] = _ptr(self.buf[f"slot_pos_{n}"])
         for name in BUFFERS[6:]:
             setattr(self.cs, name, _ptr(self.buf[name]))
-        self._ws = {}
+        self._ws, self._ws_kept = {}, []
         self.tbe = None
         if tbe:
             self.tbe_buf = {}
@@ -256,10 +256,15 @@ class ThinKVCache:
         return int(lib().thinkv_page_head_bytes(C.byref(self.layout), c))
 
     def _workspace(self, key: str, nbytes: int) -> torch.Tensor:
-        # zero-filled once: the append and decode workspaces start with arrival
-        # counters that every completed call leaves at zero
+        # zero-filled once: the append workspace starts with an arrival counter
+        # that every completed call leaves at zero.  A workspace that is too small
+        # is replaced but kept, since captured graphs write to it; the new one is at
+        # least twice as large, so that all that is kept is smaller than it.
         t = self._ws.get(key)
         if t is None or t.numel() < nbytes:
+            if t is not None:
+                self._ws_kept.append(t)
+                nbytes = max(nbytes, 2 * t.numel())
             t = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[key] = t
         return t
@@ -360,7 +365,7 @@ class ThinKVCache:
         if n == 0:
             return
         with self._guard():
-            ws = self._turnover_workspace(n, stream)
+            ws = self._turnover_workspace(stream)
             _check(self._lib.thinkv_release(self._cs_ref, self._tbe_ref, n, seq.data_ptr(), ws.data_ptr(),
                                             ws.numel(), self._raw_stream(stream)), "release")
 
@@ -372,7 +377,7 @@ class ThinKVCache:
         if n == 0:
             return
         with self._guard():
-            ws = self._turnover_workspace(n, stream)
+            ws = self._turnover_workspace(stream)
             _check(self._lib.thinkv_fork(self._cs_ref, self._tbe_ref, n, src.data_ptr(), dst.data_ptr(),
                                          ws.data_ptr(), ws.numel(), self._raw_stream(stream)), "fork")
 
@@ -399,16 +404,17 @@ class ThinKVCache:
             self._sizes[(name, args)] = n
         return n
 
-    def _turnover_workspace(self, n: int, stream) -> torch.Tensor:
-        """Its arrival counter is zeroed once, in the order of the call's stream.  The first use
+    def _turnover_workspace(self, stream) -> torch.Tensor:
+        """Of the largest call's size, so that it is never replaced: captured graphs write to it.
+        Its arrival counter is zeroed once, in the order of the call's stream.  The first use
         cannot be inside a graph capture: the zero fill would only run when the graph does."""
-        nbytes = self._sized("thinkv_turnover_workspace_bytes", n)
         t = self._ws.get("turnover")
-        if t is None or t.numel() < nbytes:
+        if t is None:
             if torch.cuda.is_current_stream_capturing():
                 raise ThinkvError(ERR_WORKSPACE, "turnover: run the call once before capturing it")
+            nbytes = self._sized("thinkv_turnover_workspace_bytes", self.max_seqs)
             with torch.cuda.stream(stream):
-                t = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self._where)
+                t = torch.zeros(nbytes, dtype=torch.uint8, device=self._where)
             self._ws["turnover"] = t
         return t
 

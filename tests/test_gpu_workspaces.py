@@ -1,0 +1,86 @@
+"""The binding's workspaces on the GPU: graphs captured before a larger call took a
+larger one."""
+import numpy as np
+import pytest
+import torch
+
+from mixed_precision_paged_thinkv_b200.binding import ThinKVCache
+
+import turnover_model as M
+from test_gpu_shared import _ids
+
+pytestmark = pytest.mark.gpu
+
+
+def _cache(lens, max_seqs, pages=2000):
+    """Sequence i with lens[i] tokens, room for max_seqs."""
+    c = ThinKVCache(8, 2, 64, 32, (8, 4, 2), max_seqs, 200, (pages,) * 3)
+    for s, n in enumerate(lens):
+        if n:
+            _append(c, [s] * n, range(n), s)
+    return c
+
+
+def _append(c, seq, pos, seed):
+    rng = np.random.default_rng(seed)
+    n = len(seq)
+    kv = torch.from_numpy(rng.standard_normal((2, n, c.H, c.d)).astype(np.float32)).half().cuda()
+    c.append(_ids(seq), _ids(pos), torch.from_numpy(rng.integers(0, 3, n).astype(np.uint8)).cuda(), kv[0], kv[1])
+
+
+def _use_freed_memory():
+    """Other tensors take, and overwrite, whatever the allocator has free."""
+    return [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda")
+            for size in (256, 512, 1024, 4096, 16384, 1 << 18, 1 << 20, 1 << 22) for _ in range(16)]
+
+
+def test_turnover_graph_outlives_a_larger_call():
+    c = _cache([300, 40], 64)
+    c.fork(_ids([0]), _ids([2]))
+    c.release(_ids([2]))
+    src, dst = _ids([0, 1]), _ids([2, 3])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.fork(src, dst)
+        c.release(dst)
+        c.fork(src, dst)
+    c.fork(_ids([0] * 50), _ids(range(10, 60)))        # needs more than the captured calls do
+    c.release(_ids(range(10, 60)))
+    taken = _use_freed_memory()
+    torch.cuda.synchronize()
+    want = M.host_buffers(c)
+    graph.replay()
+    M.fork(want, [0, 1], [2, 3], c.pool_pages)
+    M.release(want, [2, 3], c.pool_pages)
+    M.fork(want, [0, 1], [2, 3], c.pool_pages)
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    M.assert_same(M.host_buffers(c), want)
+    assert all((t == 0x5A).all() for t in taken)
+
+
+def test_append_graph_outlives_a_larger_call():
+    a, b = _cache([20] * 8, 8), _cache([20] * 8, 8)
+    seq, pos, tag = _ids(range(8)), _ids([100] * 8), torch.zeros(8, dtype=torch.uint8, device="cuda")
+    kv = torch.randn(2, 8, a.H, a.d, device="cuda").half()
+    _append(a, [0], [50], 1)
+    _append(b, [0], [50], 1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.append(seq, pos, tag, kv[0], kv[1])
+    torch.cuda.synchronize()
+    for c in (a, b):
+        _append(c, [1] * 1500, range(60, 1560), 2)
+    taken = _use_freed_memory()
+    graph.replay()
+    b.append(seq, pos, tag, kv[0], kv[1])
+    torch.cuda.synchronize()
+    assert a.status() == 0 and b.status() == 0
+    x, y = a.snapshot(), b.snapshot()
+    for name in ("num_blocks", "free_top", "fifo_head", "fifo_tail", "live_count", "num_live", "page_bump"):
+        assert np.array_equal(x[name], y[name]), name
+    for s, nb in enumerate(x["num_blocks"]):
+        assert np.array_equal(x["table"][s, :nb], y["table"][s, :nb])
+    q = torch.randn(8, a.Hq, a.d, device="cuda").half()
+    assert torch.equal(a.decode(seq, q)[0], b.decode(seq, q)[0])
+    assert all((t == 0x5A).all() for t in taken)
