@@ -255,19 +255,28 @@ class ThinKVCache:
     def page_head_bytes(self, c: int) -> int:
         return int(lib().thinkv_page_head_bytes(C.byref(self.layout), c))
 
-    def _workspace(self, key: str, nbytes: int) -> torch.Tensor:
-        # zero-filled once: the append workspace starts with an arrival counter
-        # that every completed call leaves at zero.  A workspace that is too small
-        # is replaced but kept, since captured graphs write to it; the new one is at
-        # least twice as large, so that all that is kept is smaller than it.
+    def _workspace(self, key: str, nbytes: int, stream) -> torch.Tensor:
+        # zero-filled once, in the order of the call's stream: the append workspace
+        # starts with an arrival counter that every completed call leaves at zero.
+        # A workspace that is too small is replaced but kept, since captured graphs
+        # write to it; the new one is at least twice as large, so that all that is
+        # kept is smaller than it.
         t = self._ws.get(key)
         if t is None or t.numel() < nbytes:
-            if t is not None:
-                self._ws_kept.append(t)
-                nbytes = max(nbytes, 2 * t.numel())
-            t = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+            with self._on(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    # the fill runs when the graph does: for this capture alone
+                    return torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
+                if t is not None:
+                    self._ws_kept.append(t)
+                    nbytes = max(nbytes, 2 * t.numel())
+                t = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             self._ws[key] = t
         return t
+
+    @staticmethod
+    def _on(stream):
+        return _NO_GUARD if stream is None else torch.cuda.stream(stream)
 
     # -- operations --
     def reset(self, stream=None):
@@ -284,7 +293,7 @@ class ThinKVCache:
         assert seq.dtype == torch.int32 and cls.dtype == torch.uint8 and fifo_index.dtype == torch.int32
         assert cls.numel() == n and fifo_index.numel() == n
         nbytes = int(lib().thinkv_evict_slots_workspace_bytes(n))
-        ws = self._workspace("evict_slots", nbytes)
+        ws = self._workspace("evict_slots", nbytes, stream)
         _check(lib().thinkv_evict_slots(C.byref(self.cs), n, _ptr(seq), _ptr(cls), _ptr(fifo_index),
                                         _ptr(ws), ws.numel(), _stream(stream)), "evict_slots")
 
@@ -296,7 +305,7 @@ class ThinKVCache:
         assert seq.dtype == torch.int32 and pos.dtype == torch.int32 and tag.dtype == torch.uint8
         sch = None if schedule is None else (C.c_int32 * 3)(*[int(x) for x in schedule])
         nbytes = int(lib().thinkv_tbe_workspace_bytes(n))
-        ws = self._workspace("tbe", nbytes)
+        ws = self._workspace("tbe", nbytes, stream)
         _check(lib().thinkv_evict_tbe(C.byref(self.cs), C.byref(self.tbe), n, _ptr(seq), _ptr(pos),
                                       _ptr(tag), int(t_min),
                                       None if sch is None else C.cast(sch, C.c_void_p),
@@ -311,7 +320,7 @@ class ThinKVCache:
         assert k.dtype == torch.float16 and v.dtype == torch.float16
         assert k.is_contiguous() and v.is_contiguous() and k.numel() == n * self.H * self.d
         nbytes = int(lib().thinkv_append_workspace_bytes(C.byref(self.layout), n))
-        ws = self._workspace("append", nbytes)
+        ws = self._workspace("append", nbytes, stream)
         _check(lib().thinkv_append_quantize(C.byref(self.cs), n, _ptr(seq), _ptr(pos), _ptr(tag),
                                             _ptr(k), _ptr(v), _ptr(ws), ws.numel(),
                                             _stream(stream)), "append")
@@ -330,7 +339,7 @@ class ThinKVCache:
         assert k.dtype == torch.float16 and v.dtype == torch.float16
         assert k.is_contiguous() and v.is_contiguous() and k.numel() == n * self.H * self.d
         nbytes = int(lib().thinkv_append_workspace_bytes(C.byref(self.layout), n))
-        ws = self._workspace("append", nbytes)
+        ws = self._workspace("append", nbytes, stream)
         o = None if order is None else (C.c_uint8 * 3)(*order)
         _check(lib().thinkv_append_evict(C.byref(self.cs), n, _ptr(seq), _ptr(pos), _ptr(tag),
                                          _ptr(k), _ptr(v), _ptr(budget),
@@ -353,7 +362,7 @@ class ThinKVCache:
         n = int(seq.numel())
         assert seq.dtype == torch.int32
         nbytes = int(lib().thinkv_compact_workspace_bytes(n, int(max_tokens)))
-        ws = self._workspace("compact", nbytes)
+        ws = self._workspace("compact", nbytes, stream)
         _check(lib().thinkv_compact(C.byref(self.cs), C.byref(dst.cs), n, _ptr(seq),
                                     int(max_tokens), _ptr(ws), ws.numel(), _stream(stream)),
                "compact")
@@ -410,10 +419,10 @@ class ThinKVCache:
         cannot be inside a graph capture: the zero fill would only run when the graph does."""
         t = self._ws.get("turnover")
         if t is None:
-            if torch.cuda.is_current_stream_capturing():
-                raise ThinkvError(ERR_WORKSPACE, "turnover: run the call once before capturing it")
             nbytes = self._sized("thinkv_turnover_workspace_bytes", self.max_seqs)
-            with torch.cuda.stream(stream):
+            with self._on(stream):
+                if torch.cuda.is_current_stream_capturing():
+                    raise ThinkvError(ERR_WORKSPACE, "turnover: run the call once before capturing it")
                 t = torch.zeros(nbytes, dtype=torch.uint8, device=self._where)
             self._ws["turnover"] = t
         return t
@@ -433,7 +442,7 @@ class ThinKVCache:
         nbytes = self.decode_workspace_bytes(n, int(topk or 0))
         if nbytes == 0:
             raise ThinkvError(ERR_INVALID, "decode workspace size")
-        ws = self._workspace("decode", nbytes)
+        ws = self._workspace("decode", nbytes, stream)
         _check(lib().thinkv_decode_attention(C.byref(self.cs), n, _ptr(seq), _ptr(q), _ptr(out),
                                              _ptr(mass) if topk else None, int(topk or 0),
                                              float(softmax_scale), _ptr(ws), ws.numel(),
@@ -459,12 +468,12 @@ class ThinKVCache:
             self._expect(mass, torch.float32, n * self.Hq)
         with self._guard():
             nbytes = self._sized("thinkv_decode_shared_workspace_bytes", n, topk)
-            with (_NO_GUARD if stream is None else torch.cuda.stream(stream)):
+            with self._on(stream):
                 if out is None:
                     out = torch.empty((n, self.Hq, self.d), dtype=torch.float16, device=self._where)
                 if topk and mass is None:
                     mass = torch.empty((n, self.Hq), dtype=torch.float32, device=self._where)
-                ws = self._workspace("decode_shared", nbytes)
+                ws = self._workspace("decode_shared", nbytes, stream)
             _check(self._lib.thinkv_decode_shared(
                 self._cs_ref, n, seq.data_ptr(), prefix.data_ptr(), q.data_ptr(), out.data_ptr(),
                 mass.data_ptr() if topk else None, topk, float(softmax_scale), ws.data_ptr(), ws.numel(),

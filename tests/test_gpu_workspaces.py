@@ -1,10 +1,10 @@
 """The binding's workspaces on the GPU: graphs captured before a larger call took a
-larger one."""
+larger one, first calls inside a capture, and streams given by the caller."""
 import numpy as np
 import pytest
 import torch
 
-from mixed_precision_paged_thinkv_b200.binding import ThinKVCache
+from mixed_precision_paged_thinkv_b200.binding import ThinKVCache, ThinkvError
 
 import turnover_model as M
 from test_gpu_shared import _ids
@@ -84,3 +84,59 @@ def test_append_graph_outlives_a_larger_call():
     q = torch.randn(8, a.Hq, a.d, device="cuda").half()
     assert torch.equal(a.decode(seq, q)[0], b.decode(seq, q)[0])
     assert all((t == 0x5A).all() for t in taken)
+
+
+def test_first_turnover_in_a_capture_of_the_given_stream_is_refused():
+    c = _cache([300, 40], 8)
+    dst, side, graph = _ids([2, 3]), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        graph.capture_begin()
+    try:
+        with pytest.raises(ThinkvError):               # the stream given captures, the current one does not
+            c.release(dst, stream=side)
+    finally:
+        with torch.cuda.stream(side):
+            graph.capture_end()
+    c.release(dst, stream=side)
+    side.synchronize()
+    assert c.status() == 0
+
+
+def test_first_append_in_a_capture():
+    """The graph zeroes a workspace of its own; calls outside it have theirs."""
+    a, b = _cache([], 8), _cache([], 8)
+    seq, pos, tag = _ids(range(8)), _ids([100] * 8), torch.zeros(8, dtype=torch.uint8, device="cuda")
+    kv = torch.randn(2, 8, a.H, a.d, device="cuda").half()
+    graph = torch.cuda.CUDAGraph()
+    taken = _use_freed_memory()
+    del taken
+    with torch.cuda.graph(graph):
+        a.append(seq, pos, tag, kv[0], kv[1])
+    _append(a, [3] * 20, range(20), 1)                 # before the graph ever ran
+    graph.replay()
+    _append(b, [3] * 20, range(20), 1)
+    b.append(seq, pos, tag, kv[0], kv[1])
+    q = torch.randn(8, a.Hq, a.d, device="cuda").half()
+    assert torch.equal(a.decode(seq, q)[0], b.decode(seq, q)[0])
+    assert a.status() == 0 and b.status() == 0
+    assert a.snapshot()["live_count"].tolist() == [1, 1, 1, 21, 1, 1, 1, 1]
+
+
+def test_first_append_on_a_side_stream():
+    """The zero fill of a new workspace is in the order of the stream that uses it."""
+    a, b = _cache([], 8), _cache([], 8)
+    seq, pos, tag = _ids(range(8)), _ids([100] * 8), torch.zeros(8, dtype=torch.uint8, device="cuda")
+    kv = torch.randn(2, 8, a.H, a.d, device="cuda").half()
+    side = torch.cuda.Stream()
+    b.append(seq, pos, tag, kv[0], kv[1])
+    taken = _use_freed_memory()
+    torch.cuda.synchronize()
+    del taken
+    torch.cuda._sleep(20_000_000)                      # the current stream is busy for some 10 ms
+    a.append(seq, pos, tag, kv[0], kv[1], stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    q = torch.randn(8, a.Hq, a.d, device="cuda").half()
+    assert torch.equal(a.decode(seq, q)[0], b.decode(seq, q)[0])
+    assert a.status() == 0
