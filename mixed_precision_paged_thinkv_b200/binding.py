@@ -274,6 +274,20 @@ class ThinKVCache:
             self._ws[key] = t
         return t
 
+    def _scratch(self, key: str, nbytes: int, stream, raw: int) -> torch.Tensor:
+        # of the decode calls of one stream (raw: its handle): they only read the cache
+        # and may overlap on two streams or in two graphs, so each stream has a
+        # workspace and each captured call has one of its graph's memory.  A workspace
+        # that is too small goes back to the allocator, which hands it on in the order
+        # of the stream.
+        with self._on(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(nbytes, dtype=torch.uint8, device=self._where)
+            t = self._ws.get((key, raw))
+            if t is None or t.numel() < nbytes:
+                t = self._ws[key, raw] = torch.empty(nbytes, dtype=torch.uint8, device=self._where)
+            return t
+
     @staticmethod
     def _on(stream):
         return _NO_GUARD if stream is None else torch.cuda.stream(stream)
@@ -376,7 +390,7 @@ class ThinKVCache:
         with self._guard():
             ws = self._turnover_workspace(stream)
             _check(self._lib.thinkv_release(self._cs_ref, self._tbe_ref, n, seq.data_ptr(), ws.data_ptr(),
-                                            ws.numel(), self._raw_stream(stream)), "release")
+                                            ws.numel(), _stream(stream)), "release")
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None):
         """Sequence dst[i] (empty; distinct) becomes a copy of src[i]."""
@@ -388,7 +402,7 @@ class ThinKVCache:
         with self._guard():
             ws = self._turnover_workspace(stream)
             _check(self._lib.thinkv_fork(self._cs_ref, self._tbe_ref, n, src.data_ptr(), dst.data_ptr(),
-                                         ws.data_ptr(), ws.numel(), self._raw_stream(stream)), "fork")
+                                         ws.data_ptr(), ws.numel(), _stream(stream)), "fork")
 
     def _expect(self, t: torch.Tensor, dtype, numel: int):
         assert t.dtype == dtype and t.numel() == numel and t.is_contiguous()
@@ -399,9 +413,6 @@ class ThinKVCache:
         if torch.cuda.current_device() == self._where.index:
             return _NO_GUARD
         return torch.cuda.device(self._where)
-
-    def _raw_stream(self, stream) -> int:
-        return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
     def _sized(self, name: str, *args) -> int:
         """A workspace size, asked for once per set of arguments."""
@@ -439,14 +450,12 @@ class ThinKVCache:
             out = torch.empty(n, self.Hq, self.d, dtype=torch.float16, device=self.device)
         if topk and mass is None:
             mass = torch.empty(n, self.Hq, dtype=torch.float32, device=self.device)
-        nbytes = self.decode_workspace_bytes(n, int(topk or 0))
-        if nbytes == 0:
-            raise ThinkvError(ERR_INVALID, "decode workspace size")
-        ws = self._workspace("decode", nbytes, stream)
+        nbytes = self._sized("thinkv_decode_workspace_bytes", n, int(topk or 0))
+        raw = _stream(stream)
+        ws = self._scratch("decode", nbytes, stream, raw)
         _check(lib().thinkv_decode_attention(C.byref(self.cs), n, _ptr(seq), _ptr(q), _ptr(out),
                                              _ptr(mass) if topk else None, int(topk or 0),
-                                             float(softmax_scale), _ptr(ws), ws.numel(),
-                                             _stream(stream)), "decode")
+                                             float(softmax_scale), _ptr(ws), ws.numel(), raw), "decode")
         return out, (mass if topk else None)
 
     def decode_shared_workspace_bytes(self, n: int, topk: int = 0) -> int:
@@ -457,7 +466,12 @@ class ThinKVCache:
                       topk: Optional[int] = None, softmax_scale: float = 0.0,
                       out: Optional[torch.Tensor] = None, mass: Optional[torch.Tensor] = None, stream=None):
         """Decode attention over the tokens of prefix[i] (-1: none) and of seq[i]
-        together; neighbouring rows with the same prefix read it once."""
+        together; neighbouring rows with the same prefix read it once per block of
+        256 query rows of a kv-head, where that spares enough (not with topk: then
+        every row reads its prefix itself).  Rows of such a run carry fp16 roundings
+        of keys and values, the others decode()'s; a row's bits can differ with
+        its neighbours.  Calls only read the cache: they may overlap on several
+        streams, but not with calls that change it."""
         n, topk = seq.numel(), int(topk or 0)
         self._expect(seq, torch.int32, n)
         self._expect(prefix, torch.int32, n)
@@ -473,11 +487,12 @@ class ThinKVCache:
                     out = torch.empty((n, self.Hq, self.d), dtype=torch.float16, device=self._where)
                 if topk and mass is None:
                     mass = torch.empty((n, self.Hq), dtype=torch.float32, device=self._where)
-                ws = self._workspace("decode_shared", nbytes, stream)
+            raw = _stream(stream)
+            ws = self._scratch("decode_shared", nbytes, stream, raw)
             _check(self._lib.thinkv_decode_shared(
                 self._cs_ref, n, seq.data_ptr(), prefix.data_ptr(), q.data_ptr(), out.data_ptr(),
-                mass.data_ptr() if topk else None, topk, float(softmax_scale), ws.data_ptr(), ws.numel(),
-                self._raw_stream(stream)), "decode_shared")
+                mass.data_ptr() if topk else None, topk, float(softmax_scale), ws.data_ptr(), ws.numel(), raw),
+                "decode_shared")
         return out, (mass if topk else None)
 
     def status(self, stream=None) -> int:

@@ -1,5 +1,6 @@
 """The binding's workspaces on the GPU: graphs captured before a larger call took a
-larger one, first calls inside a capture, and streams given by the caller."""
+larger one, first calls inside a capture, streams given by the caller, and
+decode calls that overlap on two streams or in two graphs."""
 import numpy as np
 import pytest
 import torch
@@ -14,10 +15,11 @@ pytestmark = pytest.mark.gpu
 
 def _cache(lens, max_seqs, pages=2000):
     """Sequence i with lens[i] tokens, room for max_seqs."""
-    c = ThinKVCache(8, 2, 64, 32, (8, 4, 2), max_seqs, 200, (pages,) * 3)
+    c = ThinKVCache(8, 2, 64, 32, (8, 4, 2), max_seqs, max([200, *(n // 16 + 4 for n in lens)]), (pages,) * 3)
     for s, n in enumerate(lens):
         if n:
             _append(c, [s] * n, range(n), s)
+    assert c.status() == 0
     return c
 
 
@@ -140,3 +142,59 @@ def test_first_append_on_a_side_stream():
     q = torch.randn(8, a.Hq, a.d, device="cuda").half()
     assert torch.equal(a.decode(seq, q)[0], b.decode(seq, q)[0])
     assert a.status() == 0
+
+
+def _decodes(c, shared, topk=None):
+    """Two calls over different rows, and what each answers alone."""
+    calls = []
+    for part in (range(2, 34), range(34, 64)):
+        seq, prefix = _ids(part), _ids([s % 2 for s in sorted(part, key=lambda s: s % 2)])
+        q = torch.randn(len(part), c.Hq, c.d, device="cuda").half()
+
+        def call(out=None, stream=None, seq=seq, prefix=prefix, q=q):
+            if shared:
+                return c.decode_shared(seq, prefix, q, topk=topk, out=out, stream=stream)[0]
+            return c.decode(seq, q, topk=topk, out=out, stream=stream)[0]
+
+        calls.append(call)
+    want = [call().clone() for call in calls]
+    torch.cuda.synchronize()
+    return calls, want
+
+
+@pytest.mark.parametrize("shared,topk", [(True, None), (True, 8), (False, None), (False, 8)])
+def test_overlapping_decodes(shared, topk):
+    c = _cache([12000, 9000] + [400] * 62, 64, pages=4000)
+    calls, want = _decodes(c, shared, topk)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty_like(w) for _ in range(40)] for w in want]
+    torch.cuda.synchronize()
+    for i in range(40):
+        for j in (0, 1):
+            calls[j](out=outs[j][i], stream=streams[j])
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    for j in (0, 1):
+        assert all(torch.equal(o, want[j]) for o in outs[j])
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_overlapping_graphs(shared):
+    """Two graphs of the same cache, replayed at the same time on two streams."""
+    c = _cache([12000, 9000] + [400] * 62, 64, pages=4000)
+    calls, want = _decodes(c, shared)
+    graphs, outs = [], []
+    for j in (0, 1):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[j]):
+            outs.append([calls[j]() for _ in range(6)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        for j in (0, 1):
+            with torch.cuda.stream(streams[j]):
+                graphs[j].replay()
+    torch.cuda.synchronize()
+    assert c.status() == 0
+    for j in (0, 1):
+        assert all(torch.equal(o, want[j]) for o in outs[j])
