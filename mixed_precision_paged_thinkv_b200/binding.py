@@ -44,6 +44,7 @@ EXPORTED = [
 ]
 
 TBE_BUFFERS = ["seg", "nseg", "settled"]
+_ALIGN_16, _ALIGN_8 = {"pool_R", "pool_E", "pool_T", "seg"}, {"block_table", "live_list"}
 
 
 class ThinkvError(RuntimeError):
@@ -195,9 +196,11 @@ class ThinKVCache:
 
     Buffers are torch tensors owned by this object; the C ABI sees raw device
     pointers.  ``bits`` are the code widths of R, E, T (default 8/4/2).
-    ``buffers``: a cache that exists already (contiguous tensors on ``device``,
-    by the names in ``BUFFERS``, and in ``TBE_BUFFERS`` with ``tbe``); it is
-    taken over as it stands, not reset.
+    ``buffers``: a cache that exists already (contiguous tensors on one device,
+    ``device``, by the names in ``BUFFERS``, and in ``TBE_BUFFERS`` with ``tbe``;
+    pools and segments start on 16-byte boundaries, lists of 64-bit entries on 8,
+    the rest on 4; those of a class without pages are left out); it is taken over
+    as it stands, not reset.
     """
 
     def __init__(self, num_q_heads: int, num_kv_heads: int, head_dim: int, group_size: int,
@@ -244,11 +247,17 @@ class ThinKVCache:
             return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes > 0 else None
         t = given.get(name)
         if nbytes == 0:
-            return t
+            return None
         if t is None or not t.is_contiguous() or t.numel() * t.element_size() != nbytes:
             raise ThinkvError(ERR_INVALID, f"buffer {name}: a contiguous tensor of {nbytes} bytes is needed")
         if t.device.type != self.device.type or self.device.index not in (None, t.device.index):
             raise ThinkvError(ERR_INVALID, f"buffer {name} is on {t.device}, not on {self.device}")
+        first = next((b for b in self.buf.values() if b is not None), t)
+        if t.device != first.device:
+            raise ThinkvError(ERR_INVALID, f"buffer {name} is on {t.device}, others are on {first.device}")
+        align = 16 if name in _ALIGN_16 else 8 if name in _ALIGN_8 else 4
+        if t.data_ptr() % align:
+            raise ThinkvError(ERR_INVALID, f"buffer {name} does not start on a {align}-byte boundary")
         return t
 
     # -- helpers --
