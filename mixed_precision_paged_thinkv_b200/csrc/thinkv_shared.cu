@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kThreads)
   const int nruns = (int)carry;
   if (tid == 0) plan.start[nruns] = n;
   __syncthreads();
-  // ---- the runs that the prefix kernel could take, and what it would spare ----
-  int64_t spared = 0, nused = 0, units = 0;
+  // ---- the runs that the prefix kernel could take, and what that would gain ----
+  int64_t gained = 0, nused = 0, units = 0;
   for (int base = 0; base < nruns; base += nt) {
     const int k = base + tid;
     int64_t v[3] = {0, 0, 0}, tot[3];
@@ -116,9 +116,13 @@ __global__ void __launch_bounds__(kThreads)
       r.pages = r.prefix >= 0 ? C.num_live[r.prefix] : 0;
       if (!inline_only && r.count >= 2 && r.pages > 0) {
         const RunShape s = run_shape(r.count, r.pages, Gq);
-        v[0] = (int64_t)(r.count - 1) * r.pages * H;
-        v[1] = 1;
-        v[2] = H * (int64_t)s.blocks * s.tiles;
+        const int64_t n_units = H * (int64_t)s.blocks * s.tiles;
+        const int64_t gain = (int64_t)(r.count - 1) * r.pages * H - kTileCost * n_units;
+        if (gain > 0) {
+          v[0] = gain;
+          v[1] = 1;
+          v[2] = n_units;
+        }
       }
     }
     const bool fit = v[1] != 0;
@@ -128,11 +132,11 @@ __global__ void __launch_bounds__(kThreads)
       plan.run[nused + v[1]] = r;
       plan.rstart[nused + v[1]] = units + v[2];
     }
-    spared += tot[0];
+    gained += tot[0];
     nused += tot[1];
     units += tot[2];
   }
-  const bool use = spared >= kWorthPageSteps;
+  const bool use = gained >= kWorthPageSteps;
   if (tid == 0) {
     plan.rstart[use ? nused : 0] = use ? units : 0;
     *plan.nruns = use ? (int)nused : 0;

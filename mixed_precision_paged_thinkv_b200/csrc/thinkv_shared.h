@@ -12,9 +12,21 @@ namespace thinkv {
 constexpr int kTilePages = 8;                 // pages of a key tile (128 tokens)
 constexpr int kBlockRows = 256;               // query rows of a prefix block, at most
 
-// Page-steps (live page x kv-head x sequence) that the split kernel has to be
-// spared before the prefix kernel is worth its own latency.
-constexpr int64_t kWorthPageSteps = 8192;
+// When the prefix kernel takes a run, in page-steps of the split kernel (live page
+// x kv-head x sequence): it spares (count - 1) * pages * H of them and costs about
+// kTileCost per unit (row block x key tile x kv-head).  Runs that spare more than
+// they cost are taken where together they gain kWorthPageSteps, which pays for the
+// launch, the start-up chain and the larger merge.  Measured, us a call, prefix kernel
+// against split kernel alone, rows x 40 own tokens on one prefix:
+//   32 q-heads, 8 kv-heads, d = 128   2 rows on 20,000 tokens 56 / 41, 4 rows 57 / 56,
+//     8 rows 59 / 87; 8 rows on 2,048 tokens 41 / 27, 32 rows 47 / 50; on 65,536 tokens
+//     2 rows 101 / 83, 3 rows 103 / 107: even at a gain of 18,000 to 31,000
+//   8 q-heads, 8 kv-heads, d = 128    11,000 to 18,000 (8 rows on 8,192 tokens 43 / 54)
+//   64 q-heads, 8 kv-heads, d = 64    28,000 to 40,000 (16 rows on 8,192 tokens 47 / 54)
+//   8 q-heads, 1 kv-head, d = 128     40,000 to 80,000 (32 rows on 20,000 tokens 71 / 60,
+//     on 65,536 tokens 77 / 138)
+constexpr int64_t kTileCost = 10;
+constexpr int64_t kWorthPageSteps = 24000;
 
 // One run of neighbours with the same prefix whose prefix goes through the
 // prefix kernel.
