@@ -28,8 +28,8 @@
 // grow to 2^15 before it is rescaled by a power of two, and starts at 2^7, so that
 // the small weights of a long flat row keep fp16's normal precision.  A rescale
 // is exact for the fp32 sums and accumulators; weights of the same tile that are
-// already stored as fp16 lose what falls below 2^-24, as if weighed under the new
-// reference at once: 2^-25 each beside a largest weight of 2^6 or more.
+// already stored as fp16 lose what falls below 2^-24, about as if weighed under the
+// new reference at once: 2^-24 each at most beside a largest weight of 2^6 or more.
 //
 // Rounding: keys, values and P enter the products as fp16, the widest type that
 // the tensor cores take at full rate beside bf16 (each key or value is one fused
@@ -271,12 +271,12 @@ template <int B, int F>
 __device__ __forceinline__ __half2 fitting(__half2 s, __half2 z) {
   const __half2 top = __hfma2(s, __float2half2_rn(largest_code<B, F>()), z);
   if (!__hble2(top, __float2half2_rn(65504.f))) {
-    auto fit = [](__half sh, __half zh) {
-      const float sf = __half2float(sh), zf = __half2float(zh);
-      const float t = fmaf(sf, largest_code<B, F>(), zf);
-      return t >= 65520.f && t < INFINITY ? __float2half_rd((65504.f - zf) / largest_code<B, F>()) : sh;
+    const float2 sf = __half22float2(s), zf = __half22float2(z);
+    auto fit = [](float sc, float ze) {
+      const float t = fmaf(sc, largest_code<B, F>(), ze);
+      return t >= 65520.f && t < INFINITY ? (65504.f - ze) * (1.f / largest_code<B, F>()) : sc;
     };
-    s = __halves2half2(fit(__low2half(s), __low2half(z)), fit(__high2half(s), __high2half(z)));
+    s = __halves2half2(__float2half_rd(fit(sf.x, zf.x)), __float2half_rd(fit(sf.y, zf.y)));
   }
   return s;
 }
@@ -494,17 +494,16 @@ __device__ __forceinline__ void scale_columns(uint32_t addr, float f) {
     tmem_st32(addr + c * 32, o);
   }
 }
-// 32 weights (fp16, 16 columns) of this thread's row, times f.  In fp32: as an fp16
-// factor f would be 0 from 2^-25 on, where weights of up to 2^15 are not.
+// 32 weights (fp16, 16 columns) of this thread's row, times f, a power of two, in
+// two steps: as one fp16 factor f would be 0 from 2^-25 on, where weights of up to
+// 2^15 are not.
 __device__ __forceinline__ void scale_weights(uint32_t addr, float f) {
   uint32_t w[16];
   tmem_ld16(addr, w);
   tc_wait_ld_of(w);
+  const __half2 f1 = __float2half2_rn(fmaxf(f, 0x1p-14f)), f2 = __float2half2_rn(fminf(f * 0x1p14f, 1.f));
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float2 v = __half22float2(as_half2(w[e]));
-    w[e] = pack_half2_rn(v.x * f, v.y * f);
-  }
+  for (int e = 0; e < 16; ++e) w[e] = as_bits(__hmul2(__hmul2(as_half2(w[e]), f1), f2));
   tmem_st16(addr, w);
 }
 
