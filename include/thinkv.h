@@ -460,20 +460,25 @@ THINKV_API size_t thinkv_decode_shared_workspace_bytes(const thinkv_layout* L, i
  * same cache (a prompt that was appended once): any sequence may be one,
  * several rows may name it, seq[i] need not differ from row to row, and a row
  * that names the same sequence twice counts its tokens twice.
- * Neighbouring rows with the same prefix[i] form a run, whose prefix is read
- * once for all of its rows; keep such rows next to each other.  (Rows with the
- * same prefix apart from each other are right as well, but read it again.)
+ * Neighbouring rows with the same prefix[i] form a run; keep such rows next to
+ * each other.  Where it gains enough (many rows, a long prefix) a run's prefix is
+ * read once per block of up to 256 query rows of a kv-head (64 rows of the call
+ * at four query heads each); elsewhere every row reads it.
  * prefix: device int32 [n_seqs].  A seq[i] or prefix[i] out of range -> *status
  * = INVALID, and that row decodes as empty.
  * topk_mass, topk: as thinkv_decode_attention, over both token lists; with it,
  * every row reads its prefix itself.
  * workspace: device, >= thinkv_decode_shared_workspace_bytes(L, n_seqs, topk)
  * bytes, no initialisation needed; calls that share it must not overlap on the
- * GPU.  Four kernels: the plan (one CTA), the prefix kernel (not launched with
- * topk_mass, nor where even full tables would make it not worth its launch; it
- * returns at once when no run of the call is), then decode's split and a merge.
- * Its rows carry fp16 roundings of keys, values and weights (thinkv_prefix.cu's
- * head), the other rows those of thinkv_decode_attention.
+ * GPU.  It holds two fp32 partial rows per row and query head where the prefix
+ * kernel may run, whatever the rows share (16,384 rows of 64 heads at d = 128:
+ * over 1 GB).  Four kernels, one after the other: the plan (one CTA), the prefix
+ * kernel (not launched with topk_mass, nor where even full tables would make it
+ * not worth its launch; it returns at once when no run of the call is), then
+ * decode's split and a merge.  Rows of a run that the prefix kernel takes carry
+ * fp16 roundings of keys, values and weights (thinkv_prefix.cu's head), the other
+ * rows those of thinkv_decode_attention: which of the two a row gets depends on
+ * its neighbours and on the lengths.
  * 1 <= n_seqs <= 16384. */
 THINKV_API int thinkv_decode_shared(const thinkv_cache* cache, int32_t n_seqs, const int32_t* seq,
                                     const int32_t* prefix, const uint16_t* q, uint16_t* out,

@@ -414,8 +414,11 @@ __device__ inline pages_t<SHARED> live_tokens(const DecodeParams& p, int i) {
 }
 
 // Warps that share T units.  SHARED: four units each at least, so that a small
-// call leaves few pieces to merge (2 rows on 2,048 tokens, 8 kv-heads: 130 pieces a
-// segment merged in 69 us before, one unit a warp; 33 pieces since).
+// call leaves few pieces to merge.  Measured with one, two, four and eight units a
+// warp at least, us a call: 2 rows on 512 tokens (32 / 8 heads, d = 128) 16.9, 16.7,
+// 17.4, 23.1; 2 rows on 2,048 tokens (64 / 8, d = 64) 26, 21, 20, 23; 2 rows on 8,192
+// tokens (4 / 2, d = 64) 55, 35, 28, 27; 16 rows of 300 own tokens on 64 (32 / 8) 19.8,
+// 19.4, 23.3, 29.2: four loses up to 4 us where lists are short, one 27 where they are not.
 template <bool SHARED>
 __device__ inline int64_t sharing_warps(int64_t T, int64_t W) {
   if constexpr (SHARED) return min(W, max(T / 4, (int64_t)1));
