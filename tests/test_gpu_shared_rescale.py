@@ -13,8 +13,9 @@ pytestmark = pytest.mark.gpu
 
 # Bound of an output element.  Keys and values are exact, products of fp16 numbers are
 # summed in fp32, and a weight is rounded to fp16 twice at most where it is rescaled
-# (2^-11 of itself each time; below fp16's normal numbers 2^-25, of weights whose
-# largest is at least 2^6: 2^-31 a key).  The fp32 exponent (scores of up to 4,096, the
+# (2^-11 of itself each time; below fp16's normal numbers 2^-25 for a factor down to
+# 2^-14, and for a smaller one, taken in two factors of which the second is 1/2 at most,
+# 2^-25 / 2 + 2^-25, beside a largest weight of at least 2^6: 1.5 * 2^-31 a key).  The fp32 exponent (scores of up to 4,096, the
 # scale is ln 2, so that a score counts powers of two: tokens that carry weight are
 # within 40 of the maximum, 40 * 2^-24 of a weight), exp2's own error (2^-22) and the
 # fp32 sums stay below 2^-17.  The output is rounded to fp16 once.
@@ -51,7 +52,7 @@ def _check(c, k, v, q, members, rel=2 * 2.0 ** -11, floor=2.0 ** -24):
         w = torch.softmax(torch.einsum("thd,hgd->hgt", kd, qd[i]) * LN2, -1)
         o = torch.einsum("hgt,thd->hgd", w, vd)
         wv = torch.einsum("hgt,thd->hgd", w, vd.abs())
-        lost = 2.0 ** -31 * torch.einsum("hgt,thd->hgd", (w > 0).double(), vd.abs())
+        lost = 1.5 * 2.0 ** -31 * torch.einsum("hgt,thd->hgd", (w > 0).double(), vd.abs())
         bound = (rel + 2.0 ** -17) * wv + torch.minimum(lost, wv) + 2.0 ** -11 * o.abs() + floor
         err = (out[i].double().view_as(o) - o).abs()
         worst = max(worst, (err / bound).max().item())
